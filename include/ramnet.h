@@ -295,6 +295,104 @@ ramnet_status ramnet_decode_step(const ramnet_config* cfg, int32_t B, int32_t H,
                                  void* y, ramnet_dtype out_dt, void* stream);
 
 /*
+ * State space layer: the operators of a layer with a dense recurrent state per head, next to
+ * the slot layer above.  A prompt runs ramnet_conv_forward, ramnet_ssm_forward and
+ * ramnet_norm_gate; a single token ramnet_conv_step, ramnet_ssm_step and ramnet_norm_gate, on
+ * the states that the prompt left.  The RAM-Net pages compare with layers of this kind but do
+ * not describe them; the definitions are those below.  Inputs are values that have already
+ * been projected.  Shapes name contiguous last dimensions; per-token inputs take element
+ * strides (as ramnet_strides) and need only element alignment, so slices of one wide
+ * projection are read in place.  Non-finite inputs spread within their head or row (in
+ * ramnet_ssm_forward also to the up to 63 tokens before them); tokens that a sequence does not
+ * have (see `lengths`) may hold anything.
+ */
+
+/* H heads of P channels with N state values per channel; head h uses the B and C vectors of
+ * group h / (H/G).  Limits: P and N in {16, 32, 64, 128, 256}, G >= 1 divides H. */
+typedef struct {
+    int32_t H, G, N, P;
+    int32_t dt_softplus;   /* 1: step size softplus(dt + dt_bias), 0: dt + dt_bias          */
+    float dt_min, dt_max;  /* clamp of the step size (0 and infinity: none of a softplus)   */
+} ramnet_ssm_config;
+
+/*
+ * ramnet_ssm_forward -- selective scan over a prompt.  Per sequence b and head h, from the
+ * state S [N,P] in S_in (zeros if NULL), for t = 0 .. lengths[b]-1:
+ *     d = clamp(softplus(dt[b,t,h] + dt_bias[h]), dt_min, dt_max)
+ *     S <- exp(d * A[h]) * S + d * Bm[b,t,g,:] (outer) x[b,t,h,:]
+ *     y[b,t,h,:] = Cm[b,t,g,:] . S + D[h] * x[b,t,h,:]
+ *
+ *   x  [B,T,H,P] in_dt, xs: its strides (NULL: dense)
+ *   dt [B,T,H]   in_dt, dts: its strides
+ *   A  [H] fp32 (negative for a decaying state);  D, dt_bias [H] fp32 or NULL (0)
+ *   Bm, Cm [B,T,G,N] in_dt, bs, cs: their strides ({b,t,g})
+ *   lengths [B] int32 or NULL (all T): tokens of each sequence, taken into [0,T].  Rows of y
+ *           behind a sequence's last token are left as they were; a sequence of length 0
+ *           hands S_in on.
+ *   S_in  [B,H,N,P] fp32 or NULL (zeros);  S_out [B,H,N,P] fp32 final state, may alias S_in
+ *   y  [B,T,H,P] out_dt, dense
+ *   workspace  device scratch of ramnet_ssm_workspace_bytes() bytes, 16-byte aligned (NULL if
+ *           that is 0); not used by other work during the call
+ * The state is fp32, and every sum has a fixed order: the same call gives the same bits.
+ * Errors: INVALID_ARG (sizes, NULL, negative strides, alignment, small workspace).
+ */
+size_t ramnet_ssm_workspace_bytes(const ramnet_ssm_config* cfg, int32_t B, int32_t T);
+ramnet_status ramnet_ssm_forward(const ramnet_ssm_config* cfg, int32_t B, int32_t T, ramnet_dtype in_dt,
+                                 const void* x, const ramnet_strides* xs, const void* dt,
+                                 const ramnet_strides* dts, const float* A, const void* Bm,
+                                 const ramnet_strides* bs, const void* Cm, const ramnet_strides* cs,
+                                 const float* D, const float* dt_bias, const int32_t* lengths,
+                                 const float* S_in, void* y, ramnet_dtype out_dt, float* S_out,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ramnet_ssm_step -- the selective scan for one token per sequence, S updated in place.
+ *   x [B,H,P], dt [B,H], Bm, Cm [B,G,N] in_dt with strides whose t is ignored (NULL: dense);
+ *   A, D, dt_bias as ramnet_ssm_forward;  S [B,H,N,P] fp32;  y [B,H,P] out_dt, dense
+ * Errors: INVALID_ARG as above.
+ */
+ramnet_status ramnet_ssm_step(const ramnet_ssm_config* cfg, int32_t B, ramnet_dtype in_dt, const void* x,
+                              const ramnet_strides* xs, const void* dt, const ramnet_strides* dts,
+                              const float* A, const void* Bm, const ramnet_strides* bs, const void* Cm,
+                              const ramnet_strides* cs, const float* D, const float* dt_bias, float* S,
+                              void* y, ramnet_dtype out_dt, void* stream);
+
+/*
+ * ramnet_conv_forward -- short causal convolution over a prompt, one filter per channel:
+ *     y[b,t,c] = act(bias[c] + sum_{k<W} w[c,k] * x[b,t-W+1+k,c]),  act = SiLU if silu != 0
+ * where the W-1 inputs before the first token come from state_in (zeros if NULL).
+ *   x [B,T,C] in_dt, element (b,t,c) at b*x_b + t*x_t + c;  w [C,W], bias [C] fp32 (or NULL)
+ *   lengths [B] int32 or NULL, as ramnet_ssm_forward
+ *   state_in, state_out [B,W-1,C] in_dt or NULL: the last W-1 inputs before and after the call;
+ *           may be the same array
+ *   y [B,T,C] out_dt, dense
+ * Limits: 2 <= W <= 4.  Errors: INVALID_ARG.
+ */
+ramnet_status ramnet_conv_forward(int32_t B, int32_t T, int32_t C, int32_t W, ramnet_dtype in_dt,
+                                  const void* x, int64_t x_b, int64_t x_t, const float* w,
+                                  const float* bias, int32_t silu, const int32_t* lengths,
+                                  const void* state_in, void* y, ramnet_dtype out_dt, void* state_out,
+                                  void* stream);
+
+/* ramnet_conv_step -- the convolution for one token per sequence: x [B,C] in_dt with element
+ * (b,c) at b*x_b + c; state [B,W-1,C] in_dt, shifted by one input in place; y [B,C] out_dt. */
+ramnet_status ramnet_conv_step(int32_t B, int32_t C, int32_t W, ramnet_dtype in_dt, const void* x,
+                               int64_t x_b, const float* w, const float* bias, int32_t silu,
+                               void* state, void* y, ramnet_dtype out_dt, void* stream);
+
+/*
+ * ramnet_norm_gate -- RMSNorm of R rows over groups of D/groups channels, with a SiLU gate:
+ *     gate_first != 0:  u = x * silu(z),  y = u / sqrt(mean_group(u^2) + eps) * w
+ *     gate_first == 0:  y = x / sqrt(mean_group(x^2) + eps) * w * silu(z)
+ *   x, z [R,D] in_dt with row strides x_r, z_r in elements (z NULL: no gate);  w [D] fp32 or
+ *   NULL (ones);  y [R,D] out_dt, dense
+ * Errors: INVALID_ARG.
+ */
+ramnet_status ramnet_norm_gate(int64_t R, int32_t D, int32_t groups, ramnet_dtype in_dt, const void* x,
+                               int64_t x_r, const void* z, int64_t z_r, const float* w, float eps,
+                               int32_t gate_first, void* y, ramnet_dtype out_dt, void* stream);
+
+/*
  * ramnet_selftest_wait_timeout -- failure-detection self-test.  The pages have no
  * counterpart: it checks this library's own guard against lost signals.  Launches one
  * block on `stream` whose bounded wait (the same routine every wait of the prefill scan

@@ -35,11 +35,12 @@ def _nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "ssm", "*.cu")))
 
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+        glob.glob(os.path.join(CSRC, "ssm", "*.cuh")) + glob.glob(os.path.join(CSRC, "ssm", "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 

@@ -7,6 +7,7 @@
 
 #include "../../include/ramnet.h"
 #include "kernels.h"
+#include "ssm/ssm.h"
 
 namespace {
 
@@ -86,6 +87,8 @@ uint32_t* device_status_ptr()
 }  // namespace
 
 namespace ramnet {
+
+uint32_t* library_status_word() { return device_status_ptr(); }
 
 // Sets the text ramnet_last_error returns on this thread (for entry points in other files).
 ramnet_status set_last_error(ramnet_status s, const char* msg)

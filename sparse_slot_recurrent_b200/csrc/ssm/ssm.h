@@ -1,0 +1,125 @@
+// ssm.h -- launch parameters and launchers of the state space layer's kernels (host side):
+// short causal convolution, selective scan, gated row norm, each as declared in
+// include/ramnet.h.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace ramnet {
+
+struct ConvParams {
+    const void* x;  // element (b, t, c) at b*sb + t*st + c
+    int64_t sb, st;
+    int in_bf16;
+    const float* w;         // [C,W]
+    const float* bias;      // [C] or null
+    int silu;
+    const int32_t* lengths;  // [B] or null (all T)
+    const void* state_in;    // [B,W-1,C] or null (zeros)
+    void* y;                 // [B,T,C]
+    int out_bf16;
+    void* state_out;  // [B,W-1,C] or null; may alias state_in
+    int B, T, C, W;
+};
+
+struct ConvStepParams {
+    const void* x;  // element (b, c) at b*sb + c
+    int64_t sb;
+    int in_bf16;
+    const float* w;
+    const float* bias;
+    int silu;
+    void* state;  // [B,W-1,C], shifted in place
+    void* y;      // [B,C]
+    int out_bf16;
+    int B, C, W;
+};
+
+// Element strides of one [B,T,H,.] operand (last dimension contiguous).
+struct Str3 {
+    int64_t b, t, h;
+};
+
+// The prompt form cuts each sequence into `nseg` segments of `seg_len` tokens that run side by
+// side: a first launch finds what each segment adds to a zero state, a second chains these
+// into the state every segment starts from, and the third computes the outputs.  With one
+// segment only the third launch runs.
+struct SsmParams {
+    const void* x;  // [B,T,H,P]
+    Str3 xs;
+    const void* dt;  // [B,T,H]
+    Str3 dts;
+    const float* A;  // [H]
+    const void* Bm;  // [B,T,G,N]
+    Str3 bs;
+    const void* Cm;  // [B,T,G,N]
+    Str3 cs;
+    int in_bf16;
+    const float* D;          // [H] or null
+    const float* dt_bias;    // [H] or null
+    const int32_t* lengths;  // [B] or null
+    const float* S_in;       // [B,H,N,P] or null
+    void* y;                 // [B,T,H,P]
+    int out_bf16;
+    float* S_out;  // [B,H,N,P]
+    int B, T, H, G, N, P;
+    int softplus;
+    float dt_min, dt_max;
+    int nseg, seg_len;
+    float* seg_state;  // [B,H,nseg,N,P]: what a segment adds, then the state it starts from
+    float* seg_decay;  // [B,H,nseg]
+    uint32_t* status;
+    uint64_t wait_ns;
+};
+
+struct SsmStepParams {
+    const void* x;  // [B,H,P]
+    Str3 xs;
+    const void* dt;  // [B,H]
+    Str3 dts;
+    const float* A;
+    const void* Bm;  // [B,G,N]
+    Str3 bs;
+    const void* Cm;
+    Str3 cs;
+    int in_bf16;
+    const float* D;
+    const float* dt_bias;
+    float* S;  // [B,H,N,P], updated in place
+    void* y;   // [B,H,P]
+    int out_bf16;
+    int B, H, G, N, P;
+    int softplus;
+    float dt_min, dt_max;
+};
+
+struct NormParams {
+    const void* x;  // element (r, d) at r*sx + d
+    int64_t sx;
+    const void* z;  // or null
+    int64_t sz;
+    int in_bf16;
+    const float* w;  // [D] or null (ones)
+    void* y;         // [R,D]
+    int out_bf16;
+    int64_t R;
+    int D, groups;
+    float eps;
+    int gate_first;
+};
+
+// Device address of the library's status word on the current device (null on a CUDA error).
+uint32_t* library_status_word();
+
+cudaError_t launch_conv(const ConvParams& p, cudaStream_t stream);
+cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t stream);
+cudaError_t launch_ssm_step(const SsmStepParams& p, cudaStream_t stream);
+cudaError_t launch_norm_gate(const NormParams& p, cudaStream_t stream);
+
+// Segments of the prompt form for these sizes; sets nseg and seg_len.
+void ssm_segments(int B, int T, int H, int N, int P, int* nseg, int* seg_len);
+cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t stream);
+
+}  // namespace ramnet

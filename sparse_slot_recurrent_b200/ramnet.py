@@ -8,7 +8,9 @@ to load, every call raises -- there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -26,6 +28,8 @@ RAMNET_F32, RAMNET_BF16 = 0, 1
 EXPORTED = ("ramnet_decode_addresses", "ramnet_scan_workspace_bytes", "ramnet_scan_layout", "ramnet_scan_forward",
             "ramnet_scan_route", "ramnet_scan_recur", "ramnet_scan_forward_noalloc", "ramnet_decode_step",
             "ramnet_scan_forward_host_scratch_bytes", "ramnet_scan_forward_host",
+            "ramnet_ssm_workspace_bytes", "ramnet_ssm_forward", "ramnet_ssm_step", "ramnet_conv_forward",
+            "ramnet_conv_step", "ramnet_norm_gate",
             "ramnet_selftest_wait_timeout", "ramnet_set_scan_wait_limit", "ramnet_sync_status", "ramnet_last_error")
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024  # RAMNET_NOALLOC_SCRATCH_BYTES
 
@@ -66,6 +70,28 @@ class Config:
 
     def _c(self) -> _Cfg:
         return _Cfg(self.d_p, self.U, self.K, self.d_v, self.eps_gsu, self.eps_norm, self.renorm)
+
+
+class _SsmCfg(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int32), ("G", ctypes.c_int32), ("N", ctypes.c_int32), ("P", ctypes.c_int32),
+                ("dt_softplus", ctypes.c_int32), ("dt_min", ctypes.c_float), ("dt_max", ctypes.c_float)]
+
+
+@dataclass(frozen=True)
+class SsmConfig:
+    """A state space layer: H heads of P channels with N state values per channel, B and C
+    vectors shared by the H/G heads of a group; step size clamp(softplus(dt + bias), dt_min, dt_max)."""
+    H: int
+    G: int
+    N: int
+    P: int
+    dt_softplus: bool = True
+    dt_min: float = 0.0
+    dt_max: float = float("inf")
+
+    def __post_init__(self):
+        c = _SsmCfg(self.H, self.G, self.N, self.P, int(self.dt_softplus), self.dt_min, self.dt_max)
+        object.__setattr__(self, "_ref", ctypes.pointer(c))
 
 
 _lib = None
@@ -114,6 +140,20 @@ def load() -> ctypes.CDLL:
     lib.ramnet_scan_forward_host.restype = ctypes.c_int
     lib.ramnet_scan_forward_host.argtypes = ([_P, _I, _I, _I, _I] + [_P] * 11 + [_I] + [_P] * 2 +
                                              [_I, _P, ctypes.c_size_t, _P])
+    SC, ST, L, D = ctypes.POINTER(_SsmCfg), ctypes.POINTER(_Strides), ctypes.c_int64, ctypes.c_int
+    lib.ramnet_ssm_workspace_bytes.restype = ctypes.c_size_t
+    lib.ramnet_ssm_workspace_bytes.argtypes = [SC, _I, _I]
+    lib.ramnet_ssm_forward.restype = ctypes.c_int
+    lib.ramnet_ssm_forward.argtypes = [SC, _I, _I, D, _P, ST, _P, ST, _P, _P, ST, _P, ST, _P, _P, _P, _P, _P, D, _P,
+                                       _P, ctypes.c_size_t, _P]
+    lib.ramnet_ssm_step.restype = ctypes.c_int
+    lib.ramnet_ssm_step.argtypes = [SC, _I, D, _P, ST, _P, ST, _P, _P, ST, _P, ST, _P, _P, _P, _P, D, _P]
+    lib.ramnet_conv_forward.restype = ctypes.c_int
+    lib.ramnet_conv_forward.argtypes = [_I, _I, _I, _I, D, _P, L, L, _P, _P, _I, _P, _P, _P, D, _P, _P]
+    lib.ramnet_conv_step.restype = ctypes.c_int
+    lib.ramnet_conv_step.argtypes = [_I, _I, _I, D, _P, L, _P, _P, _I, _P, _P, D, _P]
+    lib.ramnet_norm_gate.restype = ctypes.c_int
+    lib.ramnet_norm_gate.argtypes = [L, _I, _I, D, _P, L, _P, L, _P, ctypes.c_float, _I, _P, D, _P]
     lib.ramnet_set_scan_wait_limit.restype = ctypes.c_int
     lib.ramnet_set_scan_wait_limit.argtypes = [ctypes.c_uint32]
     lib.ramnet_sync_status.restype = ctypes.c_int
@@ -317,3 +357,180 @@ def set_scan_wait_limit(limit_us: int):
 def sync_status(stream=None):
     """Wait for the stream and raise if a kernel recorded a timeout or failed check."""
     _check(load().ramnet_sync_status(_stream(stream)))
+
+
+# ------------------------------------------------------------------ state space layer
+
+_DTYPES = {torch.bfloat16: RAMNET_BF16, torch.float32: RAMNET_F32}
+
+
+@functools.lru_cache(maxsize=1024)
+def _strides_of(b: int, t: int, h: int):
+    return ctypes.pointer(_Strides(b, t, h))
+
+
+def _arg(t, name, shape, dtype, like, dense=True):
+    """Pointer of an operand after its checks (None stays None)."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} expected")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, {dtype} expected")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, {like.device} expected")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _in(t, name):
+    """Input dtype code; the operand must be on a GPU with its last dimension contiguous."""
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    return code
+
+
+def _last_contiguous(*pairs):
+    for t, name in pairs:
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _on(t):
+    """Makes t's device current for a launch, where it is not."""
+    return contextlib.nullcontext() if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _out(y, name, shape, out_dtype, x):
+    """The output tensor (allocated if not given) and its dtype code."""
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+    elif out_dtype is not None and y.dtype != out_dtype:
+        raise TypeError(f"{name} is {y.dtype}, out_dtype is {out_dtype}")
+    code = _DTYPES.get(y.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {y.dtype}")
+    _arg(y, name, torch.Size(shape), y.dtype, x)
+    return y, code
+
+
+def ssm_workspace_bytes(cfg: SsmConfig, B: int, T: int) -> int:
+    return int(load().ramnet_ssm_workspace_bytes(cfg._ref, B, T))
+
+
+def _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias):
+    """Checked operands shared by the two forms: lead is [B] or [B, T]."""
+    lead, H, G, N = x.shape[:-2], cfg.H, cfg.G, cfg.N
+    code = _in(x, "x")
+    f32 = torch.float32
+    ptrs = (_arg(x, "x", (*lead, H, cfg.P), x.dtype, x, False), _arg(dt, "dt", (*lead, H), x.dtype, x, False),
+            _arg(A, "A", (H,), f32, x), _arg(Bm, "Bm", (*lead, G, N), x.dtype, x, False),
+            _arg(Cm, "Cm", (*lead, G, N), x.dtype, x, False), _arg(D, "D", (H,), f32, x),
+            _arg(dt_bias, "dt_bias", (H,), f32, x))
+    _last_contiguous((x, "x"), (Bm, "Bm"), (Cm, "Cm"))
+    return code, ptrs
+
+
+def ssm_forward(cfg: SsmConfig, x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=None, S_in=None, out_dtype=None, y=None,
+                S_out=None, workspace=None, stream=None):
+    """Selective scan over a prompt: x [B,T,H,P], dt [B,T,H], Bm and Cm [B,T,G,N] (bf16 or fp32, any strides
+    with the last dimension of x, Bm and Cm contiguous), A, D, dt_bias [H] fp32, lengths [B] int32.
+    Returns (y [B,T,H,P] in out_dtype (x's if None), S_out [B,H,N,P] fp32).  Rows of a y that is passed in
+    behind a sequence's last token keep their values; S_out may be S_in."""
+    B, T = x.shape[:2]
+    code, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
+    state = torch.Size((B, cfg.H, cfg.N, cfg.P))
+    plen = _arg(lengths, "lengths", (B,), torch.int32, x)
+    pin = _arg(S_in, "S_in", state, torch.float32, x)
+    y, ycode = _out(y, "y", x.shape, out_dtype, x)
+    if S_out is None:
+        S_out = torch.empty(state, dtype=torch.float32, device=x.device)
+    pout = _arg(S_out, "S_out", state, torch.float32, x)
+    if workspace is None:
+        need = ssm_workspace_bytes(cfg, B, T)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    nbytes = 0
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.device != x.device:
+            raise ValueError("workspace must be contiguous and on the device of x")
+        nbytes = workspace.numel() * workspace.element_size()
+    with _on(x):
+        _check(load().ramnet_ssm_forward(cfg._ref, B, T, code, px, _strides_of(*x.stride()[:3]), pdt,
+                                         _strides_of(*dt.stride()), pA, pB, _strides_of(*Bm.stride()[:3]), pC,
+                                         _strides_of(*Cm.stride()[:3]), pD, pbias, plen, pin, y.data_ptr(), ycode, pout,
+                                         _ptr(workspace), nbytes, _stream(stream)))
+    return y, S_out
+
+
+def ssm_step(cfg: SsmConfig, x, dt, A, Bm, Cm, S, D=None, dt_bias=None, out_dtype=None, y=None, stream=None):
+    """Selective scan for one token per sequence: x [B,H,P], dt [B,H], Bm and Cm [B,G,N]; S [B,H,N,P] fp32 is
+    updated in place.  Returns y [B,H,P]."""
+    B = x.shape[0]
+    code, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
+    pS = _arg(S, "S", (B, cfg.H, cfg.N, cfg.P), torch.float32, x)
+    y, ycode = _out(y, "y", x.shape, out_dtype, x)
+    (xb, xh, _), (db, dh), (bb, bg, _), (cb, cg, _) = x.stride(), dt.stride(), Bm.stride(), Cm.stride()
+    with _on(x):
+        _check(load().ramnet_ssm_step(cfg._ref, B, code, px, _strides_of(xb, 0, xh), pdt, _strides_of(db, 0, dh), pA, pB,
+                                      _strides_of(bb, 0, bg), pC, _strides_of(cb, 0, cg), pD, pbias, pS, y.data_ptr(),
+                                      ycode, _stream(stream)))
+    return y
+
+
+def conv_forward(x, w, bias=None, silu=True, lengths=None, state_in=None, out_dtype=None, y=None, state_out=None,
+                 stream=None):
+    """Short causal convolution over a prompt: x [B,T,C] (bf16 or fp32, channels contiguous), w [C,W] and
+    bias [C] fp32, state_in [B,W-1,C] in x's dtype (the inputs before the first token; zeros if None).
+    Returns (y [B,T,C], state_out [B,W-1,C]); state_out may be state_in."""
+    B, T, C = x.shape
+    W = w.shape[1]
+    code = _in(x, "x")
+    _last_contiguous((x, "x"))
+    pw, pb = _arg(w, "w", (C, W), torch.float32, x), _arg(bias, "bias", (C,), torch.float32, x)
+    plen = _arg(lengths, "lengths", (B,), torch.int32, x)
+    pin = _arg(state_in, "state_in", (B, W - 1, C), x.dtype, x)
+    y, ycode = _out(y, "y", x.shape, out_dtype, x)
+    if state_out is None:
+        state_out = torch.empty((B, W - 1, C), dtype=x.dtype, device=x.device)
+    pout = _arg(state_out, "state_out", (B, W - 1, C), x.dtype, x)
+    with _on(x):
+        _check(load().ramnet_conv_forward(B, T, C, W, code, x.data_ptr(), x.stride(0), x.stride(1), pw, pb, bool(silu), plen,
+                                          pin, y.data_ptr(), ycode, pout, _stream(stream)))
+    return y, state_out
+
+
+def conv_step(x, w, state, bias=None, silu=True, out_dtype=None, y=None, stream=None):
+    """The convolution for one token per sequence: x [B,C]; state [B,W-1,C] in x's dtype takes the token in
+    and drops its oldest.  Returns y [B,C]."""
+    B, C = x.shape
+    W = w.shape[1]
+    code = _in(x, "x")
+    _last_contiguous((x, "x"))
+    pw, pb = _arg(w, "w", (C, W), torch.float32, x), _arg(bias, "bias", (C,), torch.float32, x)
+    ps = _arg(state, "state", (B, W - 1, C), x.dtype, x)
+    y, ycode = _out(y, "y", x.shape, out_dtype, x)
+    with _on(x):
+        _check(load().ramnet_conv_step(B, C, W, code, x.data_ptr(), x.stride(0), pw, pb, bool(silu), ps, y.data_ptr(), ycode,
+                                       _stream(stream)))
+    return y
+
+
+def norm_gate(x, z=None, w=None, groups=1, eps=1e-6, gate_first=True, out_dtype=None, y=None, stream=None):
+    """RMSNorm of the rows of x [R,D] over ``groups`` groups of channels, times w [D] fp32, gated by silu(z)
+    (z [R,D], None: no gate) before the norm or behind it.  Returns y [R,D]."""
+    R, D = x.shape
+    code = _in(x, "x")
+    _last_contiguous((x, "x"))
+    pz = _arg(z, "z", (R, D), x.dtype, x, False)
+    if z is not None:
+        _last_contiguous((z, "z"))
+    pw = _arg(w, "w", (D,), torch.float32, x)
+    y, ycode = _out(y, "y", x.shape, out_dtype, x)
+    with _on(x):
+        _check(load().ramnet_norm_gate(R, D, groups, code, x.data_ptr(), x.stride(0), pz, 0 if z is None else z.stride(0), pw,
+                                       eps, bool(gate_first), y.data_ptr(), ycode, _stream(stream)))
+    return y

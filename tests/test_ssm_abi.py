@@ -1,0 +1,135 @@
+"""Host-side refusals of the state space layer's entry points, and of their Python binding (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+from sparse_slot_recurrent_b200 import build as build_mod
+from sparse_slot_recurrent_b200 import ramnet
+
+FAKE = 1 << 40  # 16-byte aligned, never dereferenced: every call below fails host-side
+BF, F = ramnet.RAMNET_BF16, ramnet.RAMNET_F32
+BAD = ramnet.RAMNET_ERR_INVALID_ARG
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build_mod.build()
+    return ramnet.load()
+
+
+def _cfg(**kw):
+    return ramnet.SsmConfig(**{**dict(H=4, G=2, N=64, P=64), **kw})
+
+
+def _strides(*v):
+    return None if v[0] is None else ctypes.pointer(ramnet._Strides(*v))
+
+
+def _fwd(lib, cfg=None, B=2, T=100, dt=BF, x=FAKE, xs=None, dt_ptr=FAKE, A=FAKE, Bm=FAKE, Cm=FAKE, D=None, bias=None,
+         lengths=None, S_in=None, y=FAKE, od=BF, S_out=FAKE, ws=FAKE, nbytes=1 << 40):
+    ref = (cfg or _cfg())._ref
+    return lib.ramnet_ssm_forward(ref, B, T, dt, x, xs, dt_ptr, None, A, Bm, None, Cm, None, D, bias, lengths, S_in, y, od,
+                                  S_out, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("kw", [dict(N=48), dict(N=0), dict(P=8), dict(P=512), dict(G=3), dict(G=0), dict(H=0),
+                                dict(dt_min=1.0, dt_max=0.5), dict(dt_min=float("nan"))], ids=str)
+def test_bad_layers_refused(lib, kw):
+    assert _fwd(lib, _cfg(**kw)) == BAD
+    assert ramnet.last_error() != ""
+    assert ramnet.ssm_workspace_bytes(_cfg(**kw), 2, 100) == 0
+
+
+@pytest.mark.parametrize("kw,word", [
+    (dict(B=0), "B"), (dict(T=0), "T"), (dict(B=1 << 30, T=1 << 30), "large"), (dict(dt=7), "dtype"), (dict(od=9), "dtype"),
+    (dict(x=None), "x"), (dict(x=FAKE + 1), "aligned"), (dict(dt_ptr=None), "dt"), (dict(A=None), "A"), (dict(A=FAKE + 2), "A"),
+    (dict(Bm=None), "Bm"), (dict(Cm=None), "Cm"), (dict(Cm=FAKE + 3), "Cm"), (dict(D=FAKE + 2), "D"), (dict(bias=FAKE + 1), "bias"),
+    (dict(lengths=FAKE + 2), "lengths"), (dict(S_in=FAKE + 4), "S_in"), (dict(y=None), "y"), (dict(y=FAKE + 8), "y"),
+    (dict(S_out=None), "S_out"), (dict(S_out=FAKE + 4), "S_out"), (dict(xs=_strides(100, -1, 64)), "strides"),
+    (dict(xs=_strides(1 << 62, 1, 64)), "strides")], ids=str)
+def test_bad_scan_arguments_refused(lib, kw, word):
+    assert _fwd(lib, **kw) == BAD
+    assert word in ramnet.last_error()
+
+
+def test_null_layer_refused(lib):
+    assert lib.ramnet_ssm_forward(None, 1, 1, BF, *([FAKE, None] * 2), FAKE, *([FAKE, None] * 2), None, None, None, None, FAKE, BF,
+                                  FAKE, FAKE, 1 << 40, None) == BAD
+    assert "cfg" in ramnet.last_error()
+
+
+def _step(lib, cfg=None, B=2, dt=BF, x=FAKE, S=FAKE, y=FAKE, od=BF, A=FAKE):
+    return lib.ramnet_ssm_step((cfg or _cfg())._ref, B, dt, x, None, FAKE, None, A, FAKE, None, FAKE, None, None, None, S, y, od,
+                               None)
+
+
+def test_bad_step_arguments_refused(lib):
+    for kw in (dict(cfg=_cfg(N=3)), dict(B=0), dict(dt=5), dict(od=5), dict(x=None), dict(x=FAKE + 1), dict(S=None), dict(S=FAKE + 8),
+               dict(y=FAKE + 2), dict(y=None), dict(A=None)):
+        assert _step(lib, **kw) == BAD, kw
+
+
+def _conv(lib, B=2, T=9, C=8, W=4, dt=BF, x=FAKE, xb=72, xt=8, w=FAKE, bias=None, lengths=None, si=None, y=FAKE, od=BF, so=None):
+    return lib.ramnet_conv_forward(B, T, C, W, dt, x, xb, xt, w, bias, 1, lengths, si, y, od, so, None)
+
+
+def test_bad_conv_arguments_refused(lib):
+    for kw in (dict(B=0), dict(T=0), dict(C=0), dict(W=1), dict(W=5), dict(dt=3), dict(od=3), dict(x=None), dict(x=FAKE + 1),
+               dict(xb=-1), dict(xt=-8), dict(w=None), dict(w=FAKE + 2), dict(bias=FAKE + 1), dict(lengths=FAKE + 1),
+               dict(si=FAKE + 2), dict(so=FAKE + 4), dict(y=None), dict(y=FAKE + 4), dict(B=1 << 20, C=1 << 20),
+               dict(B=1 << 16, T=1 << 16), dict(B=1 << 10, T=1 << 20, C=1 << 20)):
+        assert _conv(lib, **kw) == BAD, kw
+    step = lambda B=2, C=8, W=4, dt=BF, x=FAKE, xb=8, w=FAKE, st=FAKE, y=FAKE, od=BF: lib.ramnet_conv_step(  # noqa: E731
+        B, C, W, dt, x, xb, w, None, 1, st, y, od, None)
+    for kw in (dict(B=0), dict(C=0), dict(W=1), dict(W=5), dict(dt=3), dict(od=3), dict(x=None), dict(xb=-1), dict(w=None),
+               dict(st=None), dict(st=FAKE + 2), dict(y=None), dict(y=FAKE + 2)):
+        assert step(**kw) == BAD, kw
+
+
+def test_bad_norm_arguments_refused(lib):
+    norm = lambda R=4, D=64, groups=2, dt=BF, x=FAKE, xr=64, z=FAKE, zr=64, w=FAKE, eps=1e-6, y=FAKE, od=BF: lib.ramnet_norm_gate(  # noqa: E731
+        R, D, groups, dt, x, xr, z, zr, w, eps, 1, y, od, None)
+    for kw in (dict(R=0), dict(D=0), dict(groups=0), dict(groups=3), dict(dt=4), dict(od=4), dict(x=None), dict(x=FAKE + 1), dict(xr=-1),
+               dict(z=FAKE + 1), dict(zr=-4), dict(w=FAKE + 4), dict(eps=-1.0), dict(eps=float("nan")), dict(y=None), dict(y=FAKE + 2),
+               dict(R=1 << 31)):
+        assert norm(**kw) == BAD, kw
+
+
+def test_binding_refuses_what_the_kernels_would_misread():
+    cfg = _cfg()
+    x, dt, A = torch.zeros(2, 5, 4, 64), torch.zeros(2, 5, 4), torch.zeros(4)
+    Bm = torch.zeros(2, 5, 2, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        ramnet.ssm_forward(cfg, x, dt, A, Bm, Bm)
+    with pytest.raises(TypeError, match="dtype"):
+        ramnet.ssm_forward(cfg, x.half(), dt, A, Bm, Bm)
+    with pytest.raises(ValueError, match="CUDA"):
+        ramnet.conv_forward(torch.zeros(1, 2, 3), torch.zeros(3, 4))
+    with pytest.raises(ValueError, match="CUDA"):
+        ramnet.norm_gate(torch.zeros(2, 8))
+
+
+@pytest.mark.gpu
+def test_binding_checks_shapes_types_and_devices():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    cfg = _cfg()
+    f = dict(device="cuda")
+    x, dt, A, Bm = torch.zeros(2, 5, 4, 64, **f), torch.zeros(2, 5, 4, **f), torch.zeros(4, **f), torch.zeros(2, 5, 2, 64, **f)
+    for args, err in (((x[:, :, :3], dt, A, Bm, Bm), ValueError), ((x, dt[:, :4], A, Bm, Bm), ValueError),
+                      ((x, dt, A.double(), Bm, Bm), TypeError), ((x, dt, A.cpu(), Bm, Bm), ValueError),
+                      ((x, dt, A, Bm[:, :, :1], Bm), ValueError), ((x, dt, A, Bm.bfloat16(), Bm), TypeError),
+                      ((x.transpose(2, 3), dt, A, Bm, Bm), ValueError), ((x, dt, A[::2], Bm, Bm), ValueError)):
+        with pytest.raises(err):
+            ramnet.ssm_forward(cfg, *args)
+    with pytest.raises(TypeError):
+        ramnet.ssm_forward(cfg, x, dt, A, Bm, Bm, lengths=torch.zeros(2, dtype=torch.int64, **f))
+    with pytest.raises(ValueError):
+        ramnet.ssm_forward(cfg, x, dt, A, Bm, Bm, S_in=torch.zeros(2, 4, 64, 65, **f))
+    with pytest.raises(ValueError):
+        ramnet.conv_step(torch.zeros(2, 8, **f), torch.zeros(8, 4, **f), torch.zeros(2, 4, 8, **f))
+    with pytest.raises(ramnet.RamnetError):
+        ramnet.conv_step(torch.zeros(2, 8, **f), torch.zeros(8, 5, **f), torch.zeros(2, 4, 8, **f))
+    with pytest.raises(ramnet.RamnetError):
+        ramnet.norm_gate(torch.zeros(2, 8, **f), groups=3)
