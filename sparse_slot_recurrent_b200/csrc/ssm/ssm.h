@@ -119,7 +119,11 @@ cudaError_t launch_ssm_step(const SsmStepParams& p, cudaStream_t stream);
 cudaError_t launch_norm_gate(const NormParams& p, cudaStream_t stream);
 
 // Segments of the prompt form for these sizes; sets nseg and seg_len.
-void ssm_segments(int B, int T, int H, int N, int P, int* nseg, int* seg_len);
+void ssm_segments(int B, int T, int H, int G, int N, int P, int* nseg, int* seg_len);
 cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t stream);
+cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t stream);
+// The tensor-core form, for the types, sizes and layouts it takes.
+bool ssm_mma_takes(const SsmParams& p);
+cudaError_t launch_ssm_mma(const SsmParams& p, cudaStream_t stream);
 
 }  // namespace ramnet

@@ -76,7 +76,7 @@ size_t state_bytes(const ramnet_ssm_config* c, int64_t B) { return sizeof(float)
 
 size_t ssm_workspace(const ramnet_ssm_config* c, int32_t B, int32_t T, int* nseg, int* seg_len, size_t* decay_off)
 {
-    ramnet::ssm_segments(B, T, c->H, c->N, c->P, nseg, seg_len);
+    ramnet::ssm_segments(B, T, c->H, c->G, c->N, c->P, nseg, seg_len);
     *decay_off = 0;
     if (*nseg <= 1) return 0;
     *decay_off = state_bytes(c, B) * *nseg;

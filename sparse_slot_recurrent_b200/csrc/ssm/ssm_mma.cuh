@@ -1,0 +1,236 @@
+// ssm_mma.cuh -- device helpers of the tensor-core scan: bounded waits, tensor-map loads, tcgen05
+// descriptors and issue, and the tensor-memory and shared-memory fragment moves it uses.
+#pragma once
+
+#include <cuda.h>
+
+#include "ssm_common.cuh"
+
+namespace ramnet {
+namespace {
+
+// ------------------------------------------------------------------ bounded waits
+
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
+
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// The long part of a wait: at most kSpinLimit polls and limit_ns.  On expiry the status word gets
+// kDevTimeout and the block's abort flag is raised, after which every wait returns at once.
+__device__ __noinline__ void wait_long(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* abort_flag, uint64_t limit_ns)
+{
+    const uint64_t t_end = now_ns() + limit_ns;
+    for (uint32_t it = 0; it < kSpinLimit; ++it) {
+        if (*abort_flag) return;
+        if (try_wait(bar, parity)) return;
+        if (now_ns() > t_end) break;
+    }
+    *abort_flag = 1;
+    set_status(status, kDevTimeout);
+}
+
+__device__ __forceinline__ void arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void arrive_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ------------------------------------------------------------------ tensor-map loads (no multicast)
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------ tcgen05
+
+// Shared-memory operand in 128-byte rows with the 128-byte swizzle.  Rows of one 8-row group
+// are 128 bytes apart and groups 1024; `lbo` is the distance between 64-element blocks along
+// the row direction (used by operands whose contraction runs down the rows).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo)
+{
+    return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction word: bf16 x bf16 -> fp32, M x N; ta / tb: the operand's contraction runs down the
+// rows of shared memory (its other dimension is contiguous).
+__host__ __device__ constexpr uint32_t mma_word(int M, int N, bool ta, bool tb)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(ta) << 15) | (static_cast<uint32_t>(tb) << 16) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t word, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+// ... leaving alone the tensor-memory lanes whose bit is set in m0 (lanes 0..31) .. m3 (96..127)
+__device__ __forceinline__ void mma_ss_masked(uint32_t d, uint64_t a, uint64_t b, uint32_t word, uint32_t m0, uint32_t m1, uint32_t m2,
+                                              uint32_t m3, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %8, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(word), "r"(m0), "r"(m1), "r"(m2), "r"(m3), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+// first operand in tensor memory (two bf16 along the contraction per 32-bit column)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t word, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(word), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+// Arrives on `bar` once every MMA this thread has issued is complete.
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// 16 lanes x 16 columns: v[4k + r]: lane t/4 (+8 for r >= 2), column 8k + 2 (t%4) + r%2.
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t a, float (&v)[8])
+{
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(a));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16 lanes x 8 columns: v[2k + r]: lane t/4 + 8r, column 4k + t%4.
+__device__ __forceinline__ void tmem_st_16x8(uint32_t a, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3)
+{
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v0), "r"(v1), "r"(v2), "r"(v3) : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_x16(uint32_t a, float* v)
+{
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Placed behind tmem_wait_ld: ties the loaded registers to that point, so that no arithmetic on
+// them is moved in front of the wait.  No instruction.
+template <int N>
+__device__ __forceinline__ void settle(float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// N consecutive columns of the warp's 32 lanes.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t a, float (&v)[N])
+{
+    if constexpr (N >= 16) {
+#pragma unroll
+        for (int i = 0; i < N; i += 16) tmem_ld_x16(a + i, v + i);
+    } else {
+        tmem_ld<N>(a, v);
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t a, const uint32_t (&v)[N])
+{
+    if constexpr (N == 16)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+                     "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+                     "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                     : "memory");
+    else {
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = __uint_as_float(v[i]);
+        tmem_st<N>(a, f);
+    }
+}
+
+// ------------------------------------------------------------------ shared-memory fragments
+
+// Four 8x8 blocks of 16-bit values, transposed: lane t gets, of block k, rows 2 (t%4) and +1 of
+// column t/4; `addr`: lane 8k + r points at row r of block k.
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t (&v)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void stsm_t(uint32_t addr, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v0), "r"(v1), "r"(v2), "r"(v3)
+                 : "memory");
+}
+
+// ------------------------------------------------------------------ values as bf16 pieces
+
+__device__ __forceinline__ float bf_lo(uint32_t pair) { return __uint_as_float(pair << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
+
+__device__ __forceinline__ uint32_t pack_rn(float a, float b)  // a in the low half
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+// The leading 8 bits of a and b as one pair, and what is left of them.
+__device__ __forceinline__ uint32_t peel(float& a, float& b)
+{
+    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+    a -= __uint_as_float(ua & 0xffff0000u);
+    b -= __uint_as_float(ub & 0xffff0000u);
+    return __byte_perm(ua, ub, 0x7632);
+}
+
+}  // namespace
+}  // namespace ramnet

@@ -137,8 +137,8 @@ cudaError_t go(const SsmParams& p, cudaStream_t s)
     const unsigned gx = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * (p.P / pt));
     if (p.nseg > 1) {
         k_ssm_scan<N, false><<<dim3(gx, p.nseg - 1), threads, smem, s>>>(p);
-        const int64_t n = static_cast<int64_t>(p.B) * p.H * p.N * p.P;
-        k_ssm_chain<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(p);
+        const cudaError_t e = launch_ssm_chain(p, s);
+        if (e != cudaSuccess) return e;
     }
     k_ssm_scan<N, true><<<dim3(gx, p.nseg), threads, smem, s>>>(p);
     return cudaGetLastError();
@@ -146,15 +146,28 @@ cudaError_t go(const SsmParams& p, cudaStream_t s)
 
 }  // namespace
 
-void ssm_segments(int B, int T, int H, int N, int P, int* nseg, int* seg_len)
+cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t s)
 {
-    (void)B, (void)H, (void)N, (void)P;
-    *nseg = 1;
-    *seg_len = T;
+    const int64_t n = static_cast<int64_t>(p.B) * p.H * p.N * p.P;
+    k_ssm_chain<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+void ssm_segments(int B, int T, int H, int G, int N, int P, int* nseg, int* seg_len)
+{
+    (void)N;
+    const int64_t units = static_cast<int64_t>(B) * G * ((H / G * P + 127) / 128);
+    int64_t n = units > 0 ? 148 / units : 1;
+    const int64_t most = T / 256;
+    n = n < most ? n : most;
+    if (n < 1) n = 1;
+    *seg_len = static_cast<int>(((T + n - 1) / n + 63) / 64 * 64);
+    *nseg = (T + *seg_len - 1) / *seg_len;
 }
 
 cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t s)
 {
+    if (ssm_mma_takes(p)) return launch_ssm_mma(p, s);
     switch (p.N) {
         case 16: return go<16>(p, s);
         case 32: return go<32>(p, s);

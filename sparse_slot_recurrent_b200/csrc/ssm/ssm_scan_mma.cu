@@ -1,0 +1,612 @@
+// ssm_scan_mma.cu -- selective scan over a prompt on the tensor cores (bf16 in and out):
+//   S_t = exp(d_t A) S_{t-1} + d_t B_t (x) x_t,   y_t = C_t . S_t + D x_t.
+//
+// Mathematics.  Over a chunk of 64 tokens with a_i = sum_{k<=i} d_k A, from the state S before it,
+//   y_i  = exp(a_i) C_i . S  +  sum_{j<=i} exp(a_i - a_j) d_j (C_i . B_j) x_j  +  D x_i
+//   S'   = exp(a_63) S + sum_j (exp(a_63 - a_j) d_j x_j) (x) B_j
+// so a chunk is four products.  All are taken transposed, with 128 channels p of one group's heads
+// (128/P heads) down the 128 lanes of tensor memory:
+//   G^T [j,i] = B C^T             both from shared memory, M = 64
+//   Yb  [p,i] = S^T C^T           S^T in tensor memory as two bf16 pieces
+//   Ya  [p,i] = X^T W^T           W[i,j] = exp(a_i - a_j) d_j G[i,j], two bf16 pieces in shared memory,
+//                                 one product per head with the other heads' lanes switched off
+//   dS  [p,n] = Xw^T B            Xw = exp(a_63 - a_j) d_j x_j in tensor memory, three bf16 pieces
+// and y^T = exp(a_i) Yb + Ya + D x^T.  The tiles of x, B and C are used as they arrive by TMA, B and C in
+// both roles; x is transposed on the way to registers (ldmatrix.trans) and y on the way back.
+//
+// Precision.  The state itself stays in fp32 registers and takes dS with one fused multiply-add
+// per chunk (the tensor core's accumulation would shave a bit off a long-lived state every
+// chunk).  Xw is exact in three pieces of 8 bits; S and W as operands of a bf16 result carry 16
+// bits, 2^-16 of each value against the result's 2^-9.  Sums of d A are taken in 64 bits; a_i - a_j is the
+// difference of two float pairs, so strong decay early in a chunk costs later tokens nothing.
+//
+// Work split.  One CTA per (sequence, 128 channels, segment of the sequence), chunks in order; 16
+// warps do the elementwise work of a chunk, each on 32 channels x 16 tokens (or N/4 state columns), one
+// warp feeds TMA, one issues MMAs, one computes step sizes and decays.  Per chunk the order
+//   W -> [MMA Ya] Xw -> [MMA dS] y -> [MMA G of the next chunk] S -> [MMA Yb] ...
+// puts elementwise work of the same warps behind every MMA's latency.
+// Bound: issue slots of the elementwise work (about 500 instructions per warp and chunk).
+#include <mutex>
+
+#include "ssm_mma.cuh"
+
+namespace ramnet {
+namespace {
+
+constexpr int kQ = 64;           // tokens per chunk
+constexpr int kWarps = 16;       // elementwise warps
+constexpr int kThreads = (kWarps + 3) * 32;
+constexpr int kStgPitch = 80;    // bytes per token row of a warp's y patch: 64 used; conflict-free
+constexpr size_t kSmemMax = 232448 - 1024;  // the rest: barriers
+
+// per (stage, head) step sizes and decays of a chunk
+struct Tok {
+    float4 t[kQ];    // a_j log2(e) as a float pair, d_j, exp(a_63 - a_j) d_j
+    float hi[kQ], lo[kQ];  // the same pair, by token
+    float ein[kQ];   // exp(a_i)
+    float w[kQ];     // exp(a_63 - a_j) d_j
+    float dec, pad[3];     // exp(a_63)
+};
+
+enum Bar { kLanded = 0, kToks = 4, kEmpty = 8, kFixed = 12, kG, kW, kY, kYfree, kS, kXw, kDs = kXw + 2, kDrain = kDs + 2, kBars };
+
+struct Layout {
+    int stages;
+    uint32_t b_off, c_off, stage_bytes, w_off, stg_off, tok_off, total;
+};
+
+__host__ __device__ constexpr Layout layout_of(int N, int HP, bool out)
+{
+    const uint32_t nt = (N + 63) / 64 * 8192u;
+    Layout l{};
+    l.b_off = 16384;
+    l.c_off = l.b_off + nt;
+    l.stage_bytes = l.c_off + (out ? nt : 0);
+    const uint32_t fixed = (out ? HP * 16384u + kWarps * 16 * kStgPitch : 0);
+    l.stages = 4;
+    while (l.stages > 2 && l.stages * (l.stage_bytes + HP * sizeof(Tok)) + fixed + 1024 > kSmemMax) --l.stages;
+    l.w_off = l.stages * l.stage_bytes;
+    l.stg_off = l.w_off + (out ? HP * 16384u : 0);
+    l.tok_off = l.stg_off + (out ? kWarps * 16 * kStgPitch : 0);
+    l.total = l.tok_off + l.stages * HP * static_cast<uint32_t>(sizeof(Tok)) + 1024;  // 1024: base alignment
+    return l;
+}
+
+__device__ __forceinline__ float ex2(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+struct MmaMaps {
+    CUtensorMap x, b, c;
+};
+
+// N state values, HP heads per 128 channels; OUT: outputs and final state, else what a segment adds to a
+// zero state.
+template <int N, int HP, bool OUT>
+__global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__ MmaMaps maps, const SsmParams p, int tiles)
+{
+    constexpr Layout L = layout_of(N, HP, OUT);
+    constexpr int NB = OUT ? 1 : 2;  // buffers of Xw and dS
+    constexpr uint32_t cDs = 0, cShi = N, cSlo = N + N / 2, cXw = 256, cYb = 352, cYa = 416;  // tensor-memory columns
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(8) uint64_t bar_mem[kBars];
+    __shared__ uint32_t tmem_holder;
+    __shared__ int abort_mem;
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t s0 = smem_addr(sm), bars = smem_addr(bar_mem);
+    Tok* toks = reinterpret_cast<Tok*>(sm + L.tok_off);
+    volatile int* abort_flag = &abort_mem;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // which channels and tokens
+    const int tile = static_cast<int>(blockIdx.x % tiles);
+    const int bg = static_cast<int>(blockIdx.x / tiles);
+    const int g = bg % p.G, b = bg / p.G, seg = blockIdx.y;
+    const int hg = p.H / p.G, c0 = tile * 128, cend = hg * p.P;  // channels [c0, min(c0+128, cend)) of the group
+    const SegRange r = seg_range(seq_len(p.lengths, b, p.T), seg, p.seg_len);
+    const int nch = (r.last - r.first + kQ - 1) / kQ;
+    const int head0 = c0 / p.P;  // first head, within the group
+
+    auto bar = [&](int i) { return bars + 8u * i; };
+    auto wait = [&](int i, uint32_t parity) {
+        if (!try_wait(bars + 8u * i, parity)) wait_long(bars + 8u * i, parity, p.status, abort_flag, p.wait_ns);
+    };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar_mem + kLanded + i, 1);
+            mbar_init(bar_mem + kToks + i, 1);
+            mbar_init(bar_mem + kEmpty + i, kWarps);
+        }
+        mbar_init(bar_mem + kFixed, 1);
+        mbar_init(bar_mem + kG, 1);
+        mbar_init(bar_mem + kDrain, 1);
+        mbar_init(bar_mem + kW, kWarps);
+        mbar_init(bar_mem + kY, 1);
+        mbar_init(bar_mem + kYfree, kWarps);
+        mbar_init(bar_mem + kS, kWarps);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar_mem + kXw + i, kWarps);
+            mbar_init(bar_mem + kDs + i, 1);
+        }
+        abort_mem = 0;
+        fence_mbar_init_cluster();
+    }
+    if (warp == kWarps) tmem_alloc(&tmem_holder, 512);
+    if (OUT) {  // the blocks of W above its diagonal stay zero
+        uint4* w = reinterpret_cast<uint4*>(sm + L.w_off);
+        for (uint32_t i = threadIdx.x; i < HP * 1024u; i += kThreads) w[i] = make_uint4(0, 0, 0, 0);
+        fence_async_smem();
+    }
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    const uint32_t tm = tmem_holder;
+
+    if (warp < kWarps) {
+        // ------------------------------------------------------------ elementwise warps
+        const int q = warp & 3, cb = warp >> 2;
+        const uint32_t tq = tm + (static_cast<uint32_t>(q) << 21);  // this warp's 32 lanes
+        const int hw = HP == 4 ? q : HP == 2 ? q >> 1 : 0;          // head of its channels
+        const int ch = c0 + q * 32 + lane;                          // channel of state column work
+        const bool mine = ch < cend;
+        const int64_t bh = static_cast<int64_t>(b) * p.H + g * hg + ch / p.P;
+        const int64_t np = static_cast<int64_t>(N) * p.P;
+        const int pc = ch % p.P;
+        const float skip = (OUT && p.D && mine) ? p.D[g * hg + (c0 + q * 32) / p.P] : 0.0f;
+        constexpr int NC = N / 4;  // state columns per warp
+        float S[NC];
+        {
+            const float* from = nullptr;
+            if (OUT && mine) {
+                if (p.nseg > 1) from = p.seg_state + (bh * p.nseg + seg) * np;
+                else if (p.S_in) from = p.S_in + bh * np;
+            }
+#pragma unroll
+            for (int k = 0; k < NC; ++k) S[k] = from ? from[static_cast<int64_t>(cb * NC + k) * p.P + pc] : 0.0f;
+        }
+        auto put_state = [&]() {
+            uint32_t hi[NC / 2], lo[NC / 2];
+#pragma unroll
+            for (int k = 0; k < NC / 2; ++k) {
+                float u = S[2 * k], v = S[2 * k + 1];
+                hi[k] = peel(u, v);
+                lo[k] = pack_rn(u, v);
+            }
+            tmem_st_cols<NC / 2>(tq + cShi + cb * (NC / 2), hi);
+            tmem_st_cols<NC / 2>(tq + cSlo + cb * (NC / 2), lo);
+            tmem_wait_st();
+        };
+        auto done = [&](int i) {  // this warp's part of hand-over i
+            tmem_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive(bar(i));
+        };
+        if (OUT && nch > 0) {
+            put_state();
+            done(kS);
+        }
+        // ldmatrix row of this lane: token cb*16 + row, 8 channels; and of the y patch
+        const int row = 8 * (lane >> 4) + (lane & 7), pcol = 8 * ((lane >> 3) & 1);
+        const int jrow = cb * 16 + row;
+        uint32_t xaddr[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int pp = q * 32 + half * 16 + pcol;
+            xaddr[half] = s0 + (pp >> 6) * 8192 + jrow * 128 + ((((pp & 63) >> 3) ^ (jrow & 7)) << 4);
+        }
+        const uint32_t patch = s0 + L.stg_off + warp * 16 * kStgPitch;
+        auto sum_state = [&](int c) {  // S' = dec S + dS
+            const int i = NB == 2 ? c & 1 : 0;
+            wait(kDs + i, NB == 2 ? (c >> 1) & 1 : c & 1);
+            tmem_fence_after_sync();
+            float d[NC];
+            tmem_ld_cols<NC>(tq + cDs + i * N + cb * NC, d);
+            const float dec = toks[(c % L.stages) * HP + hw].dec;
+            tmem_wait_ld();
+            settle(d);
+#pragma unroll
+            for (int k = 0; k < NC; ++k) S[k] = fmaf(S[k], dec, d[k]);
+        };
+        for (int c = 0; c < nch; ++c) {
+            const int st = c % L.stages;
+            const uint32_t ph = (c / L.stages) & 1;
+            const int nv = min(kQ, r.last - r.first - c * kQ);
+            const Tok* tok = toks + st * HP;
+            wait(kToks + st, ph);
+            wait(kLanded + st, ph);
+            if (nv < kQ) wait(kFixed, 0);
+            if constexpr (OUT) {
+                wait(kG, c & 1);
+                tmem_fence_after_sync();
+                if (cb >= q) {  // tokens j of block q reach tokens i of block cb
+                    float gv[8];
+                    tmem_ld_16x16(tq + cYa + cb * 16, gv);
+                    const int j = q * 16 + (lane >> 2), i = cb * 16 + 2 * (lane & 3);
+                    tmem_wait_ld();
+                    settle(gv);
+#pragma unroll
+                    for (int h = 0; h < HP; ++h) {
+                        const Tok& tk = tok[h];
+                        const uint32_t wbase = L.w_off + h * 16384;
+#pragma unroll
+                        for (int rb = 0; rb < 2; ++rb) {
+                            const float4 tj = tk.t[j + 8 * rb];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int ii = i + 8 * k;
+                                const float2 hi = *reinterpret_cast<const float2*>(tk.hi + ii);
+                                const float2 lo = *reinterpret_cast<const float2*>(tk.lo + ii);
+                                float u = gv[4 * k + 2 * rb] * (tj.z * ex2((hi.x - tj.x) + (lo.x - tj.y)));
+                                float v = gv[4 * k + 2 * rb + 1] * (tj.z * ex2((hi.y - tj.x) + (lo.y - tj.y)));
+                                if (cb == q) {
+                                    u = ii >= j + 8 * rb ? u : 0.0f;
+                                    v = ii + 1 >= j + 8 * rb ? v : 0.0f;
+                                }
+                                const uint32_t at = wbase + (j + 8 * rb) * 128 + ((((ii >> 3)) ^ (j & 7)) << 4) + (ii & 7) * 2;
+                                const uint32_t wh = peel(u, v);
+                                *reinterpret_cast<uint32_t*>(sm + at) = wh;
+                                *reinterpret_cast<uint32_t*>(sm + at + 8192) = pack_rn(u, v);
+                            }
+                        }
+                    }
+                    fence_async_smem();
+                }
+                done(kW);
+            }
+            // Xw: this warp's 32 channels x 16 tokens, three exact pieces
+            uint32_t x[2][4];
+            {
+                const uint32_t xw = tq + cXw + (NB == 2 ? (c & 1) * 96 : 0) + cb * 8;
+                const float* w = tok[hw].w + cb * 16 + 2 * (lane & 3);
+                const float2 w0 = *reinterpret_cast<const float2*>(w), w1 = *reinterpret_cast<const float2*>(w + 8);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    ldsm_t(xaddr[half] + st * L.stage_bytes, x[half]);
+                    uint32_t piece[3][4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 ww = k < 2 ? w0 : w1;
+                        float u = bf_lo(x[half][k]) * ww.x, v = bf_hi(x[half][k]) * ww.y;
+                        piece[0][k] = peel(u, v);
+                        piece[1][k] = peel(u, v);
+                        piece[2][k] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
+                    }
+#pragma unroll
+                    for (int s = 0; s < 3; ++s)
+                        tmem_st_16x8(xw + (static_cast<uint32_t>(half) << 20) + s * 32, piece[s][0], piece[s][1], piece[s][2], piece[s][3]);
+                }
+                tmem_wait_st();
+                done(kXw + (NB == 2 ? c & 1 : 0));
+            }
+            if constexpr (OUT) {
+                // y of this warp's 32 channels x 16 tokens
+                const float* e = tok[hw].ein + cb * 16 + 2 * (lane & 3);
+                const float2 e0 = *reinterpret_cast<const float2*>(e), e1 = *reinterpret_cast<const float2*>(e + 8);
+                wait(kY, c & 1);
+                tmem_fence_after_sync();
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float yb[8], ya[8];
+                    tmem_ld_16x16(tq + (static_cast<uint32_t>(half) << 20) + cYb + cb * 16, yb);
+                    tmem_ld_16x16(tq + (static_cast<uint32_t>(half) << 20) + cYa + cb * 16, ya);
+                    tmem_wait_ld();
+                    settle(yb);
+                    settle(ya);
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // 8 tokens k/2, 8 channels k%2
+                        const int at = 4 * (k >> 1) + 2 * (k & 1);
+                        const float2 ee = k < 2 ? e0 : e1;
+                        const float u = fmaf(skip, bf_lo(x[half][k]), fmaf(ee.x, yb[at], ya[at]));
+                        const float v = fmaf(skip, bf_hi(x[half][k]), fmaf(ee.y, yb[at + 1], ya[at + 1]));
+                        o[k] = pack_rn(u, v);
+                    }
+                    stsm_t(patch + row * kStgPitch + (half * 16 + pcol) * 2, o[0], o[1], o[2], o[3]);
+                }
+                done(kYfree);
+                const int cc = c0 + q * 32 + (lane & 3) * 8;
+#pragma unroll
+                for (int it = 0; it < 2; ++it) {
+                    const int rr = (lane >> 2) + 8 * it, tl = cb * 16 + rr;
+                    const uint4 v = *reinterpret_cast<const uint4*>(sm + L.stg_off + warp * 16 * kStgPitch + rr * kStgPitch + (lane & 3) * 16);
+                    if (tl < nv && cc < cend)
+                        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.y) +
+                                                  ((static_cast<int64_t>(b) * p.T + r.first + c * kQ + tl) * p.H + g * hg) * p.P + cc) = v;
+                }
+                sum_state(c);
+                if (c + 1 < nch) {
+                    put_state();
+                    done(kS);
+                }
+                __syncwarp();
+                if (lane == 0) arrive(bar(kEmpty + st));
+            } else if (c > 0) {
+                sum_state(c - 1);
+                __syncwarp();
+                if (lane == 0) arrive(bar(kEmpty + (c - 1) % L.stages));
+            }
+        }
+        if (!OUT && nch > 0) sum_state(nch - 1);
+        float* to = nullptr;
+        if (mine) {
+            if (!OUT) to = p.seg_state + (bh * p.nseg + seg) * np;
+            else if (seg == p.nseg - 1) to = p.S_out + bh * np;
+        }
+        if (to) {
+#pragma unroll
+            for (int k = 0; k < NC; ++k) to[static_cast<int64_t>(cb * NC + k) * p.P + pc] = S[k];
+        }
+    } else if (warp == kWarps) {
+        // ------------------------------------------------------------ TMA
+        int issued = 0;
+        for (int c = 0; c < nch; ++c) {
+            const int st = c % L.stages;
+            if (c >= L.stages) wait(kEmpty + st, ((c / L.stages) - 1) & 1);
+            if (*abort_flag) break;
+            const int t0 = r.first + c * kQ, nv = min(kQ, r.last - t0);
+            const uint32_t base = s0 + st * L.stage_bytes;
+            if (lane == 0) {
+                arrive_tx(bar(kLanded + st), L.stage_bytes);
+                tma_load_3d(base, &maps.x, g * cend + c0, t0, b, bar(kLanded + st));
+                tma_load_3d(base + 8192, &maps.x, g * cend + c0 + 64, t0, b, bar(kLanded + st));
+#pragma unroll
+                for (int k = 0; k < (N + 63) / 64; ++k) {
+                    tma_load_4d(base + L.b_off + k * 8192, &maps.b, k * 64, g, t0, b, bar(kLanded + st));
+                    if (OUT) tma_load_4d(base + L.c_off + k * 8192, &maps.c, k * 64, g, t0, b, bar(kLanded + st));
+                }
+            }
+            issued = c + 1;
+            if (nv < kQ) {
+                // rows behind the sequence may hold anything: zeros in their place
+                wait(kLanded + st, (c / L.stages) & 1);
+                for (uint32_t i = lane; i < L.stage_bytes / 16; i += 32)
+                    if (static_cast<int>((i >> 3) & 63) >= nv) *reinterpret_cast<uint4*>(sm + st * L.stage_bytes + i * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(bar(kFixed));
+            }
+        }
+        // no copy may land in this block's memory after it has gone (bounded, also after an abort)
+        if (*abort_flag && lane == 0) {
+            const uint64_t t_end = now_ns() + 2000000000ull;
+            for (int c = issued > L.stages ? issued - L.stages : 0; c < issued; ++c)
+                for (uint32_t it = 0; it < kSpinLimit; ++it)
+                    if (try_wait(bar(kLanded + c % L.stages), (c / L.stages) & 1) || now_ns() > t_end) break;
+        }
+    } else if (warp == kWarps + 1) {
+        // ------------------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr uint32_t wG = mma_word(64, 64, false, false), wYb = mma_word(128, 64, false, false);
+            constexpr uint32_t wYa = mma_word(128, 64, true, true), wDs = mma_word(128, N, false, true);
+            for (int c = 0; c < nch; ++c) {
+                const int st = c % L.stages;
+                const uint32_t base = s0 + st * L.stage_bytes;
+                wait(kLanded + st, (c / L.stages) & 1);
+                if (r.last - r.first - c * kQ < kQ) wait(kFixed, 0);
+                if (*abort_flag) break;
+                if constexpr (OUT) {
+                    if (c > 0) wait(kYfree, (c - 1) & 1);
+                    tmem_fence_after_sync();
+#pragma unroll
+                    for (int k = 0; k < N / 16; ++k)
+                        mma_ss(tm + cYa, smem_desc(base + L.b_off + (k >> 2) * 8192 + (k & 3) * 32, 16),
+                               smem_desc(base + L.c_off + (k >> 2) * 8192 + (k & 3) * 32, 16), wG, k > 0);
+                    mma_commit(bar(kG));
+                    wait(kS, c & 1);
+                    tmem_fence_after_sync();
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int k = 0; k < N / 16; ++k)
+                            mma_ts(tm + cYb, tm + (s ? cShi : cSlo) + k * 8, smem_desc(base + L.c_off + (k >> 2) * 8192 + (k & 3) * 32, 16),
+                                   wYb, s + k > 0);
+                    wait(kW, c & 1);
+                    tmem_fence_after_sync();
+#pragma unroll
+                    for (int h = 0; h < HP; ++h)
+#pragma unroll
+                        for (int s = 0; s < 2; ++s)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint64_t da = smem_desc(base + k * 2048, 8192);
+                                const uint64_t db = smem_desc(s0 + L.w_off + h * 16384 + (s ? 0 : 8192) + k * 2048, 8192);
+                                if (HP == 1) mma_ss(tm + cYa, da, db, wYa, s + k > 0);
+                                else {
+                                    auto off = [&](int qq) { return (HP == 4 ? qq : qq >> 1) == h ? 0u : 0xffffffffu; };
+                                    mma_ss_masked(tm + cYa, da, db, wYa, off(0), off(1), off(2), off(3), s + k > 0);
+                                }
+                            }
+                    mma_commit(bar(kY));
+                }
+                const int i = NB == 2 ? c & 1 : 0;
+                wait(kXw + i, NB == 2 ? (c >> 1) & 1 : c & 1);
+                tmem_fence_after_sync();
+#pragma unroll
+                for (int s = 2; s >= 0; --s)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(tm + cDs + i * N, tm + cXw + i * 96 + s * 32 + k * 8, smem_desc(base + L.b_off + k * 2048, 8192), wDs,
+                               s < 2 || k > 0);
+                mma_commit(bar(kDs + i));
+            }
+            if (*abort_flag) {  // tensor memory is given back only when nothing writes to it
+                const uint64_t t_end = now_ns() + 2000000000ull;
+                mma_commit(bar(kDrain));
+                for (uint32_t it = 0; it < kSpinLimit; ++it)
+                    if (try_wait(bar(kDrain), 0) || now_ns() > t_end) break;
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ step sizes and decays
+        double seg_log[HP];
+#pragma unroll
+        for (int h = 0; h < HP; ++h) seg_log[h] = 0.0;
+        for (int c = 0; c < nch; ++c) {
+            const int st = c % L.stages;
+            if (c >= L.stages) wait(kEmpty + st, ((c / L.stages) - 1) & 1);
+            if (*abort_flag) break;
+            const int t0 = r.first + c * kQ;
+#pragma unroll
+            for (int h = 0; h < HP; ++h) {
+                const int hl = head0 + h, hh = g * hg + hl;
+                const bool real = hl < hg;
+                const float A = real ? p.A[hh] : 0.0f, bias = (real && p.dt_bias) ? p.dt_bias[hh] : 0.0f;
+                float d[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int t = t0 + 2 * lane + k;
+                    d[k] = 0.0f;  // a token that is not there neither decays nor writes
+                    if (real && t < r.last)
+                        d[k] = step_size(load_in(p.dt, static_cast<size_t>(b * p.dts.b + t * p.dts.t + hh * p.dts.h), 1), bias, p.softplus,
+                                         p.dt_min, p.dt_max);
+                }
+                const double a0 = static_cast<double>(d[0]) * A, a1 = static_cast<double>(d[1]) * A;
+                double sum = a0 + a1;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const double up = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += up;
+                }
+                const double total = __shfl_sync(0xffffffffu, sum, 31);
+                Tok& tk = toks[st * HP + h];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const double cum = k ? sum : sum - a1;
+                    const double l2 = cum * 1.4426950408889634074;
+                    const float hi = static_cast<float>(l2), lo = static_cast<float>(l2 - static_cast<double>(hi));
+                    const float w = d[k] * expf(static_cast<float>(total - cum));
+                    const int j = 2 * lane + k;
+                    tk.t[j] = make_float4(hi, lo, d[k], w);
+                    tk.hi[j] = hi;
+                    tk.lo[j] = lo;
+                    tk.ein[j] = expf(static_cast<float>(cum));
+                    tk.w[j] = w;
+                }
+                if (lane == 0) tk.dec = static_cast<float>(exp(total));
+                seg_log[h] += total;
+            }
+            __syncwarp();
+            if (lane == 0) arrive(bar(kToks + st));
+        }
+        if (!OUT && lane == 0) {
+#pragma unroll
+            for (int h = 0; h < HP; ++h)
+                if (head0 + h < hg && c0 % p.P == 0)
+                    p.seg_decay[(static_cast<int64_t>(b) * p.H + g * hg + head0 + h) * p.nseg + seg] = static_cast<float>(exp(seg_log[h]));
+        }
+    }
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    if (warp == kWarps) tmem_dealloc(tm, 512);
+}
+
+// ------------------------------------------------------------------ host side
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder()
+{
+    static EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// 64 tokens x 64 elements of a bf16 operand: dims inner (contiguous), then (size, stride in elements).
+bool encode(CUtensorMap* map, const void* base, int rank, const int64_t* size, const int64_t* stride)
+{
+    cuuint64_t dims[4], bytes[3];
+    cuuint32_t box[4], one[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        dims[i] = static_cast<cuuint64_t>(size[i]);
+        box[i] = i == 0 || i == rank - 2 ? 64 : 1;
+        // the stride of a single element is never used
+        if (i > 0) bytes[i - 1] = size[i] == 1 ? 16 : static_cast<cuuint64_t>(stride[i]) * 2;
+    }
+    return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, bytes, box, one,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_operands(const SsmParams& p, MmaMaps* m)
+{
+    const int64_t xsize[3] = {static_cast<int64_t>(p.H) * p.P, p.T, p.B}, xstr[3] = {1, p.xs.t, p.xs.b};
+    const int64_t bsize[4] = {p.N, p.G, p.T, p.B}, bstr[4] = {1, p.bs.h, p.bs.t, p.bs.b}, cstr[4] = {1, p.cs.h, p.cs.t, p.cs.b};
+    return encode(&m->x, p.x, 3, xsize, xstr) && encode(&m->b, p.Bm, 4, bsize, bstr) && encode(&m->c, p.Cm, 4, bsize, cstr);
+}
+
+template <int N, int HP, bool OUT>
+cudaError_t go(const SsmParams& p, const MmaMaps& m, int tiles, int segs, cudaStream_t s)
+{
+    constexpr Layout L = layout_of(N, HP, OUT);
+    static_assert(L.total <= kSmemMax, "shared memory");
+    auto kern = k_ssm_mma<N, HP, OUT>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L.total));
+    if (e != cudaSuccess) return e;
+    kern<<<dim3(static_cast<unsigned>(p.B) * p.G * tiles, segs), kThreads, L.total, s>>>(m, p, tiles);
+    return cudaGetLastError();
+}
+
+template <int N, int HP>
+cudaError_t all(const SsmParams& p, const MmaMaps& m, cudaStream_t s)
+{
+    const int tiles = (p.H / p.G * p.P + 127) / 128;
+    if (p.nseg > 1) {
+        cudaError_t e = go<N, HP, false>(p, m, tiles, p.nseg - 1, s);
+        if (e == cudaSuccess) e = launch_ssm_chain(p, s);
+        if (e != cudaSuccess) return e;
+    }
+    return go<N, HP, true>(p, m, tiles, p.nseg, s);
+}
+
+template <int N>
+cudaError_t pick(const SsmParams& p, const MmaMaps& m, cudaStream_t s)
+{
+    if (p.P == 32) return all<N, 4>(p, m, s);
+    if (p.P == 64) return all<N, 2>(p, m, s);
+    return all<N, 1>(p, m, s);
+}
+
+bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+// TMA wants strides of whole 16 bytes below 2^40; a stride of nothing (an expanded view) is left out
+bool ok_stride(int64_t n, int64_t size) { return size == 1 || (n > 0 && n % 8 == 0 && n < (1ll << 39)); }
+
+}  // namespace
+
+bool ssm_mma_takes(const SsmParams& p)
+{
+    if (!p.in_bf16 || !p.out_bf16 || p.P < 32 || p.N > 128) return false;
+    if (!al16(p.x) || !al16(p.Bm) || !al16(p.Cm)) return false;
+    if (p.H > 1 && p.xs.h != p.P) return false;  // heads side by side: one row of channels per token
+    if (!ok_stride(p.xs.t, p.T) || !ok_stride(p.xs.b, p.B)) return false;
+    if (!ok_stride(p.bs.h, p.G) || !ok_stride(p.bs.t, p.T) || !ok_stride(p.bs.b, p.B)) return false;
+    if (!ok_stride(p.cs.h, p.G) || !ok_stride(p.cs.t, p.T) || !ok_stride(p.cs.b, p.B)) return false;
+    return encoder() != nullptr;
+}
+
+cudaError_t launch_ssm_mma(const SsmParams& p, cudaStream_t s)
+{
+    MmaMaps m;
+    if (!map_operands(p, &m)) return cudaErrorInvalidValue;
+    switch (p.N) {
+        case 16: return pick<16>(p, m, s);
+        case 32: return pick<32>(p, m, s);
+        case 64: return pick<64>(p, m, s);
+        case 128: return pick<128>(p, m, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace ramnet
