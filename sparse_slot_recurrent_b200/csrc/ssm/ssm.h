@@ -42,10 +42,17 @@ struct Str3 {
     int64_t b, t, h;
 };
 
-// The prompt form cuts each sequence into `nseg` segments of `seg_len` tokens that run side by
-// side: a first launch finds what each segment adds to a zero state, a second chains these
-// into the state every segment starts from, and the third computes the outputs.  With one
-// segment only the third launch runs.
+// How the prompt form cuts each sequence: `nseg` segments of `seg_len` tokens run side by side.  A
+// first launch finds what each piece of the sequence before the last segment adds to a zero state
+// (`sub` pieces per segment), a second chains these into the states the segments start from, and
+// the third computes the outputs.  With one segment only the third launch runs.
+struct SsmSplit {
+    int nseg, seg_len, sub;
+    __host__ __device__ int pieces() const { return (nseg - 1) * sub; }
+    __host__ __device__ int piece_len() const { return seg_len / sub; }
+    __host__ __device__ int slots() const { return pieces() + 1; }  // states per (sequence, head) in the workspace
+};
+
 struct SsmParams {
     const void* x;  // [B,T,H,P]
     Str3 xs;
@@ -67,9 +74,9 @@ struct SsmParams {
     int B, T, H, G, N, P;
     int softplus;
     float dt_min, dt_max;
-    int nseg, seg_len;
-    float* seg_state;  // [B,H,nseg,N,P]: what a segment adds, then the state it starts from
-    float* seg_decay;  // [B,H,nseg]
+    SsmSplit split;
+    float* seg_state;  // [B,H,slots,N,P]: what piece i adds; then, in slot k*sub, the state segment k starts from
+    float* seg_decay;  // [B,H,pieces]
     uint32_t* status;
     uint64_t wait_ns;
 };
@@ -118,8 +125,7 @@ cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t stream);
 cudaError_t launch_ssm_step(const SsmStepParams& p, cudaStream_t stream);
 cudaError_t launch_norm_gate(const NormParams& p, cudaStream_t stream);
 
-// Segments of the prompt form for these sizes; sets nseg and seg_len.
-void ssm_segments(int B, int T, int H, int G, int N, int P, int* nseg, int* seg_len);
+SsmSplit ssm_split(int B, int T, int H, int G, int P);
 cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t stream);
 cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t stream);
 // The tensor-core form, for the types, sizes and layouts it takes.

@@ -74,13 +74,13 @@ bool take_strides(const ramnet_strides* s, int64_t B, int64_t T, int64_t H, int6
 
 size_t state_bytes(const ramnet_ssm_config* c, int64_t B) { return sizeof(float) * B * c->H * c->N * c->P; }
 
-size_t ssm_workspace(const ramnet_ssm_config* c, int32_t B, int32_t T, int* nseg, int* seg_len, size_t* decay_off)
+size_t ssm_workspace(const ramnet_ssm_config* c, int32_t B, int32_t T, ramnet::SsmSplit* split, size_t* decay_off)
 {
-    ramnet::ssm_segments(B, T, c->H, c->G, c->N, c->P, nseg, seg_len);
+    *split = ramnet::ssm_split(B, T, c->H, c->G, c->P);
     *decay_off = 0;
-    if (*nseg <= 1) return 0;
-    *decay_off = state_bytes(c, B) * *nseg;
-    return *decay_off + sizeof(float) * static_cast<size_t>(B) * c->H * *nseg;
+    if (split->nseg <= 1) return 0;
+    *decay_off = state_bytes(c, B) * split->slots();
+    return *decay_off + sizeof(float) * static_cast<size_t>(B) * c->H * split->pieces();
 }
 
 }  // namespace
@@ -91,9 +91,9 @@ size_t ramnet_ssm_workspace_bytes(const ramnet_ssm_config* cfg, int32_t B, int32
 {
     ramnet::set_last_error(RAMNET_OK, "");
     if (check_ssm(cfg, B, T) != RAMNET_OK) return 0;
-    int nseg, seg_len;
+    ramnet::SsmSplit split;
     size_t off;
-    return ssm_workspace(cfg, B, T, &nseg, &seg_len, &off);
+    return ssm_workspace(cfg, B, T, &split, &off);
 }
 
 ramnet_status ramnet_ssm_forward(const ramnet_ssm_config* cfg, int32_t B, int32_t T, ramnet_dtype in_dt, const void* x,
@@ -125,7 +125,7 @@ ramnet_status ramnet_ssm_forward(const ramnet_ssm_config* cfg, int32_t B, int32_
     NEED(y, 16);
     NEED(S_out, 16);
     size_t off;
-    const size_t need = ssm_workspace(cfg, B, T, &p.nseg, &p.seg_len, &off);
+    const size_t need = ssm_workspace(cfg, B, T, &p.split, &off);
     if (need > 0) {
         NEED(workspace, 16);
         CHECK(workspace_bytes >= need, "workspace of %zu bytes, %zu needed", workspace_bytes, need);

@@ -92,34 +92,53 @@ __host__ __device__ constexpr uint32_t mma_word(int M, int N, bool ta, bool tb)
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t word, bool add)
+// The two halves of a descriptor: the address moves within the low word, the high word is fixed.
+struct Desc {
+    uint32_t lo, hi;
+    __device__ __forceinline__ Desc operator+(uint32_t bytes) const { return Desc{lo + (bytes >> 4), hi}; }
+};
+__device__ __forceinline__ Desc desc_of(uint32_t addr, uint32_t lbo)
+{
+    const uint64_t d = smem_desc(addr, lbo);
+    return Desc{static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, Desc a, Desc b, uint32_t word, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(word), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
 
 // ... leaving alone the tensor-memory lanes whose bit is set in m0 (lanes 0..31) .. m3 (96..127)
-__device__ __forceinline__ void mma_ss_masked(uint32_t d, uint64_t a, uint64_t b, uint32_t word, uint32_t m0, uint32_t m1, uint32_t m2,
-                                              uint32_t m3, bool add)
+__device__ __forceinline__ void mma_ss_masked(uint32_t d, Desc a, Desc b, uint32_t word, uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3,
+                                              bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %8, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%4, %5, %6, %7}, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(word), "r"(m0), "r"(m1), "r"(m2), "r"(m3), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, {%7, %8, %9, %10}, p;\n\t}" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(m0), "r"(m1), "r"(m2), "r"(m3)
         : "memory");
 }
 
 // first operand in tensor memory (two bf16 along the contraction per 32-bit column)
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t word, bool add)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t word, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(word), "r"(static_cast<uint32_t>(add))
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add))
         : "memory");
+}
+
+// One lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
 
 // Arrives on `bar` once every MMA this thread has issued is complete.

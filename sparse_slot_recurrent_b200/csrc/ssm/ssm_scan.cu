@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(128) k_ssm_scan(SsmParams p)
     const int h = static_cast<int>(bh % p.H);
     const int64_t b = bh / p.H;
     const int g = h / (p.H / p.G);
-    const SegRange r = seg_range(seq_len(p.lengths, static_cast<int>(b), p.T), seg, p.seg_len);
+    const SegRange r = seg_range(seq_len(p.lengths, static_cast<int>(b), p.T), seg, OUT ? p.split.seg_len : p.split.piece_len());
     const int s = threadIdx.x % NS, pl = threadIdx.x / NS;
     const int ch = tile * pt + pl;
     const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f, skip = p.D ? p.D[h] : 0.0f;
@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(128) k_ssm_scan(SsmParams p)
     float S[16];
     const float* start = nullptr;
     if (OUT) {
-        if (p.nseg > 1) start = p.seg_state + (bh * p.nseg + seg) * static_cast<int64_t>(N) * p.P;
+        if (p.split.nseg > 1) start = p.seg_state + (bh * p.split.slots() + seg * p.split.sub) * static_cast<int64_t>(N) * p.P;
         else if (p.S_in) start = p.S_in + bh * static_cast<int64_t>(N) * p.P;
     }
 #pragma unroll
@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(128) k_ssm_scan(SsmParams p)
         }
     }
     float* end = nullptr;
-    if (!OUT) end = p.seg_state + (bh * p.nseg + seg) * static_cast<int64_t>(N) * p.P;
-    else if (seg == p.nseg - 1) end = p.S_out + bh * static_cast<int64_t>(N) * p.P;
+    if (!OUT) end = p.seg_state + (bh * p.split.slots() + seg) * static_cast<int64_t>(N) * p.P;
+    else if (seg == p.split.nseg - 1) end = p.S_out + bh * static_cast<int64_t>(N) * p.P;
     if (end) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
@@ -107,24 +107,29 @@ __global__ void __launch_bounds__(128) k_ssm_scan(SsmParams p)
         }
     }
     if (!OUT && threadIdx.x == 0 && tile == 0)
-        p.seg_decay[bh * p.nseg + seg] = static_cast<float>(exp(logdecay));
+        p.seg_decay[bh * p.split.pieces() + seg] = static_cast<float>(exp(logdecay));
 }
 
-// Turns what each segment adds into the state it starts from, in token order.
+// Turns what the pieces add into the states the segments start from, in token order; four
+// neighbouring state values per thread, one (sequence, head) per blockIdx.y.
 __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
 {
-    const int64_t np = static_cast<int64_t>(p.N) * p.P;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= static_cast<int64_t>(p.B) * p.H * np) return;
-    const int64_t bh = i / np, e = i % np;
-    float s = p.S_in ? p.S_in[i] : 0.0f;
-    for (int k = 0; k < p.nseg; ++k) {
-        float* at = p.seg_state + (bh * p.nseg + k) * np + e;
-        // the last segment's own contribution is not needed, and was not computed
-        const float add = k + 1 < p.nseg ? *at : 0.0f;
-        *at = s;
-        if (k + 1 < p.nseg) s = fmaf(p.seg_decay[bh * p.nseg + k], s, add);
+    const int np4 = p.N * p.P / 4;
+    const int e = blockIdx.x * 256 + threadIdx.x;
+    if (e >= np4) return;
+    const int64_t bh = blockIdx.y;
+    float4 s = p.S_in ? reinterpret_cast<const float4*>(p.S_in)[bh * np4 + e] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float4* at = reinterpret_cast<float4*>(p.seg_state) + bh * p.split.slots() * np4 + e;
+    const float* decay = p.seg_decay + bh * p.split.pieces();
+    const int n = p.split.pieces(), sub = p.split.sub;
+#pragma unroll 4
+    for (int k = 0; k < n; ++k, at += np4) {
+        const float4 add = *at;
+        const float d = decay[k];
+        if (k % sub == 0) *at = s;
+        s = make_float4(fmaf(d, s.x, add.x), fmaf(d, s.y, add.y), fmaf(d, s.z, add.z), fmaf(d, s.w, add.w));
     }
+    *at = s;
 }
 
 template <int N>
@@ -135,12 +140,12 @@ cudaError_t go(const SsmParams& p, cudaStream_t s)
     const int pt = threads / NS;
     const size_t smem = sizeof(float) * (2 * kTok * N + kTok * pt + 2 * kTok);
     const unsigned gx = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * (p.P / pt));
-    if (p.nseg > 1) {
-        k_ssm_scan<N, false><<<dim3(gx, p.nseg - 1), threads, smem, s>>>(p);
+    if (p.split.nseg > 1) {
+        k_ssm_scan<N, false><<<dim3(gx, p.split.pieces()), threads, smem, s>>>(p);
         const cudaError_t e = launch_ssm_chain(p, s);
         if (e != cudaSuccess) return e;
     }
-    k_ssm_scan<N, true><<<dim3(gx, p.nseg), threads, smem, s>>>(p);
+    k_ssm_scan<N, true><<<dim3(gx, p.split.nseg), threads, smem, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -148,21 +153,34 @@ cudaError_t go(const SsmParams& p, cudaStream_t s)
 
 cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t s)
 {
-    const int64_t n = static_cast<int64_t>(p.B) * p.H * p.N * p.P;
-    k_ssm_chain<<<static_cast<unsigned>((n + 255) / 256), 256, 0, s>>>(p);
+    const int64_t bh = static_cast<int64_t>(p.B) * p.H;
+    for (int64_t at = 0; at < bh; at += 65535) {  // the grid's limit in y
+        SsmParams q = p;
+        const int64_t np = static_cast<int64_t>(p.N) * p.P;
+        if (p.S_in) q.S_in = p.S_in + at * np;
+        q.seg_state = p.seg_state + at * p.split.slots() * np;
+        q.seg_decay = p.seg_decay + at * p.split.pieces();
+        const int64_t rows = bh - at < 65535 ? bh - at : 65535;
+        k_ssm_chain<<<dim3(static_cast<unsigned>((np / 4 + 255) / 256), static_cast<unsigned>(rows)), 256, 0, s>>>(q);
+    }
     return cudaGetLastError();
 }
 
-void ssm_segments(int B, int T, int H, int G, int N, int P, int* nseg, int* seg_len)
+// As many segments as fill 148 SMs with one block of 128 channels each, none shorter than 256
+// tokens; and where the segments before the last leave SMs idle in the first launch, pieces of them.
+SsmSplit ssm_split(int B, int T, int H, int G, int P)
 {
-    (void)N;
-    const int64_t units = static_cast<int64_t>(B) * G * ((H / G * P + 127) / 128);
-    int64_t n = units > 0 ? 148 / units : 1;
+    const int64_t units = static_cast<int64_t>(B) * G * ((static_cast<int64_t>(H / G) * P + 127) / 128);
+    int64_t n = 148 / units;
     const int64_t most = T / 256;
     n = n < most ? n : most;
-    if (n < 1) n = 1;
-    *seg_len = static_cast<int>(((T + n - 1) / n + 63) / 64 * 64);
-    *nseg = (T + *seg_len - 1) / *seg_len;
+    SsmSplit s{1, T, 1};
+    if (n <= 1) return s;
+    s.seg_len = static_cast<int>((T + n - 1) / n + 63) / 64 * 64;
+    s.nseg = (T + s.seg_len - 1) / s.seg_len;
+    if (s.nseg <= 1) return SsmSplit{1, T, 1};
+    while (units * (s.nseg - 1) * s.sub * 2 <= 148 && s.seg_len % (128 * s.sub) == 0) s.sub *= 2;
+    return s;
 }
 
 cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t s)

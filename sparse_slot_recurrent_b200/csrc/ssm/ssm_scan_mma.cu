@@ -35,7 +35,8 @@ namespace {
 
 constexpr int kQ = 64;           // tokens per chunk
 constexpr int kWarps = 16;       // elementwise warps
-constexpr int kThreads = (kWarps + 3) * 32;
+constexpr int kDtWarps = 2;      // warps that compute step sizes and decays, in alternate chunks
+constexpr int kThreads = (kWarps + 2 + kDtWarps) * 32;
 constexpr int kStgPitch = 80;    // bytes per token row of a warp's y patch: 64 used; conflict-free
 constexpr size_t kSmemMax = 232448 - 1024;  // the rest: barriers
 
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     __shared__ __align__(8) uint64_t bar_mem[kBars];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_mem;
+    __shared__ double log_mem[kDtWarps][HP];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t s0 = smem_addr(sm), bars = smem_addr(bar_mem);
     Tok* toks = reinterpret_cast<Tok*>(sm + L.tok_off);
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     const int bg = static_cast<int>(blockIdx.x / tiles);
     const int g = bg % p.G, b = bg / p.G, seg = blockIdx.y;
     const int hg = p.H / p.G, c0 = tile * 128, cend = hg * p.P;  // channels [c0, min(c0+128, cend)) of the group
-    const SegRange r = seg_range(seq_len(p.lengths, b, p.T), seg, p.seg_len);
+    const SegRange r = seg_range(seq_len(p.lengths, b, p.T), seg, OUT ? p.split.seg_len : p.split.piece_len());
     const int nch = (r.last - r.first + kQ - 1) / kQ;
     const int head0 = c0 / p.P;  // first head, within the group
 
@@ -162,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         {
             const float* from = nullptr;
             if (OUT && mine) {
-                if (p.nseg > 1) from = p.seg_state + (bh * p.nseg + seg) * np;
+                if (p.split.nseg > 1) from = p.seg_state + (bh * p.split.slots() + seg * p.split.sub) * np;
                 else if (p.S_in) from = p.S_in + bh * np;
             }
 #pragma unroll
@@ -199,21 +201,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             xaddr[half] = s0 + (pp >> 6) * 8192 + jrow * 128 + ((((pp & 63) >> 3) ^ (jrow & 7)) << 4);
         }
         const uint32_t patch = s0 + L.stg_off + warp * 16 * kStgPitch;
-        auto sum_state = [&](int c) {  // S' = dec S + dS
+        auto sum_state = [&](int c, const Tok* tok) {  // S' = dec S + dS
             const int i = NB == 2 ? c & 1 : 0;
             wait(kDs + i, NB == 2 ? (c >> 1) & 1 : c & 1);
             tmem_fence_after_sync();
             float d[NC];
             tmem_ld_cols<NC>(tq + cDs + i * N + cb * NC, d);
-            const float dec = toks[(c % L.stages) * HP + hw].dec;
+            const float dec = tok[hw].dec;
             tmem_wait_ld();
             settle(d);
 #pragma unroll
             for (int k = 0; k < NC; ++k) S[k] = fmaf(S[k], dec, d[k]);
         };
+        // this lane's 16 bytes of y: token cb*16 + lane/4 (+8), 8 channels
+        const int ycol = c0 + q * 32 + (lane & 3) * 8, ytok = cb * 16 + (lane >> 2);
+        const int64_t yrow = static_cast<int64_t>(p.H) * p.P;
+        __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.T + r.first + ytok) * yrow + g * cend + ycol;
+        int st = 0;
+        uint32_t ph = 0;
         for (int c = 0; c < nch; ++c) {
-            const int st = c % L.stages;
-            const uint32_t ph = (c / L.stages) & 1;
             const int nv = min(kQ, r.last - r.first - c * kQ);
             const Tok* tok = toks + st * HP;
             wait(kToks + st, ph);
@@ -308,16 +314,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     stsm_t(patch + row * kStgPitch + (half * 16 + pcol) * 2, o[0], o[1], o[2], o[3]);
                 }
                 done(kYfree);
-                const int cc = c0 + q * 32 + (lane & 3) * 8;
 #pragma unroll
                 for (int it = 0; it < 2; ++it) {
-                    const int rr = (lane >> 2) + 8 * it, tl = cb * 16 + rr;
-                    const uint4 v = *reinterpret_cast<const uint4*>(sm + L.stg_off + warp * 16 * kStgPitch + rr * kStgPitch + (lane & 3) * 16);
-                    if (tl < nv && cc < cend)
-                        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.y) +
-                                                  ((static_cast<int64_t>(b) * p.T + r.first + c * kQ + tl) * p.H + g * hg) * p.P + cc) = v;
+                    const uint4 v = *reinterpret_cast<const uint4*>(sm + L.stg_off + (warp * 16 + (lane >> 2) + 8 * it) * kStgPitch + (lane & 3) * 16);
+                    if (ytok + 8 * it < nv && ycol < cend) *reinterpret_cast<uint4*>(yp + it * 8 * yrow) = v;
                 }
-                sum_state(c);
+                yp += kQ * yrow;
+                sum_state(c, tok);
                 if (c + 1 < nch) {
                     put_state();
                     done(kS);
@@ -325,16 +328,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                 __syncwarp();
                 if (lane == 0) arrive(bar(kEmpty + st));
             } else if (c > 0) {
-                sum_state(c - 1);
+                const int before = st == 0 ? L.stages - 1 : st - 1;
+                sum_state(c - 1, toks + before * HP);
                 __syncwarp();
-                if (lane == 0) arrive(bar(kEmpty + (c - 1) % L.stages));
+                if (lane == 0) arrive(bar(kEmpty + before));
             }
+            if (++st == L.stages) st = 0, ph ^= 1;
         }
-        if (!OUT && nch > 0) sum_state(nch - 1);
+        if (!OUT && nch > 0) sum_state(nch - 1, toks + (st == 0 ? L.stages - 1 : st - 1) * HP);
         float* to = nullptr;
         if (mine) {
-            if (!OUT) to = p.seg_state + (bh * p.nseg + seg) * np;
-            else if (seg == p.nseg - 1) to = p.S_out + bh * np;
+            if (!OUT) to = p.seg_state + (bh * p.split.slots() + seg) * np;
+            else if (seg == p.split.nseg - 1) to = p.S_out + bh * np;
         }
         if (to) {
 #pragma unroll
@@ -378,94 +383,122 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     if (try_wait(bar(kLanded + c % L.stages), (c / L.stages) & 1) || now_ns() > t_end) break;
         }
     } else if (warp == kWarps + 1) {
-        // ------------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            constexpr uint32_t wG = mma_word(64, 64, false, false), wYb = mma_word(128, 64, false, false);
-            constexpr uint32_t wYa = mma_word(128, 64, true, true), wDs = mma_word(128, N, false, true);
-            for (int c = 0; c < nch; ++c) {
-                const int st = c % L.stages;
-                const uint32_t base = s0 + st * L.stage_bytes;
-                wait(kLanded + st, (c / L.stages) & 1);
-                if (r.last - r.first - c * kQ < kQ) wait(kFixed, 0);
-                if (*abort_flag) break;
-                if constexpr (OUT) {
-                    if (c > 0) wait(kYfree, (c - 1) & 1);
-                    tmem_fence_after_sync();
+        // ------------------------------------------------------------ MMA issue (whole warp, one lane issues)
+        constexpr uint32_t wG = mma_word(64, 64, false, false), wYb = mma_word(128, 64, false, false);
+        constexpr uint32_t wYa = mma_word(128, 64, true, true), wDs = mma_word(128, N, false, true);
+        const Desc wdesc = desc_of(s0 + L.w_off, 8192);
+        int st = 0;
+        uint32_t ph = 0;
+        for (int c = 0; c < nch; ++c) {
+            const Desc down = desc_of(s0 + st * L.stage_bytes, 8192);  // contraction down the rows: x, B as [j, n]
+            const Desc along = desc_of(s0 + st * L.stage_bytes, 16);   // contraction along the rows: B and C as [., n]
+            wait(kLanded + st, ph);
+            if (r.last - r.first - c * kQ < kQ) wait(kFixed, 0);
+            if (*abort_flag) break;
+            if constexpr (OUT) {
+                if (c > 0) wait(kYfree, (c - 1) & 1);
+                tmem_fence_after_sync();
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < N / 16; ++k)
-                        mma_ss(tm + cYa, smem_desc(base + L.b_off + (k >> 2) * 8192 + (k & 3) * 32, 16),
-                               smem_desc(base + L.c_off + (k >> 2) * 8192 + (k & 3) * 32, 16), wG, k > 0);
+                        mma_ss(tm + cYa, along + (L.b_off + (k >> 2) * 8192 + (k & 3) * 32), along + (L.c_off + (k >> 2) * 8192 + (k & 3) * 32),
+                               wG, k > 0);
                     mma_commit(bar(kG));
-                    wait(kS, c & 1);
-                    tmem_fence_after_sync();
+                }
+                __syncwarp();
+                wait(kS, c & 1);
+                tmem_fence_after_sync();
+                if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < 2; ++s)
 #pragma unroll
                         for (int k = 0; k < N / 16; ++k)
-                            mma_ts(tm + cYb, tm + (s ? cShi : cSlo) + k * 8, smem_desc(base + L.c_off + (k >> 2) * 8192 + (k & 3) * 32, 16),
-                                   wYb, s + k > 0);
-                    wait(kW, c & 1);
-                    tmem_fence_after_sync();
+                            mma_ts(tm + cYb, tm + (s ? cShi : cSlo) + k * 8, along + (L.c_off + (k >> 2) * 8192 + (k & 3) * 32), wYb, s + k > 0);
+                }
+                __syncwarp();
+                wait(kW, c & 1);
+                tmem_fence_after_sync();
+                if (elect_one()) {
 #pragma unroll
                     for (int h = 0; h < HP; ++h)
 #pragma unroll
                         for (int s = 0; s < 2; ++s)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const uint64_t da = smem_desc(base + k * 2048, 8192);
-                                const uint64_t db = smem_desc(s0 + L.w_off + h * 16384 + (s ? 0 : 8192) + k * 2048, 8192);
-                                if (HP == 1) mma_ss(tm + cYa, da, db, wYa, s + k > 0);
-                                else {
+                                const Desc da = down + k * 2048, db = wdesc + (h * 16384 + (s ? 0 : 8192) + k * 2048);
+                                if constexpr (HP == 1) {
+                                    mma_ss(tm + cYa, da, db, wYa, s + k > 0);
+                                } else {
                                     auto off = [&](int qq) { return (HP == 4 ? qq : qq >> 1) == h ? 0u : 0xffffffffu; };
                                     mma_ss_masked(tm + cYa, da, db, wYa, off(0), off(1), off(2), off(3), s + k > 0);
                                 }
                             }
                     mma_commit(bar(kY));
                 }
-                const int i = NB == 2 ? c & 1 : 0;
-                wait(kXw + i, NB == 2 ? (c >> 1) & 1 : c & 1);
-                tmem_fence_after_sync();
+                __syncwarp();
+            }
+            const int i = NB == 2 ? c & 1 : 0;
+            wait(kXw + i, NB == 2 ? (c >> 1) & 1 : c & 1);
+            tmem_fence_after_sync();
+            if (elect_one()) {
 #pragma unroll
                 for (int s = 2; s >= 0; --s)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ts(tm + cDs + i * N, tm + cXw + i * 96 + s * 32 + k * 8, smem_desc(base + L.b_off + k * 2048, 8192), wDs,
-                               s < 2 || k > 0);
+                        mma_ts(tm + cDs + i * N, tm + cXw + i * 96 + s * 32 + k * 8, down + (L.b_off + k * 2048), wDs, s < 2 || k > 0);
                 mma_commit(bar(kDs + i));
             }
-            if (*abort_flag) {  // tensor memory is given back only when nothing writes to it
-                const uint64_t t_end = now_ns() + 2000000000ull;
-                mma_commit(bar(kDrain));
-                for (uint32_t it = 0; it < kSpinLimit; ++it)
-                    if (try_wait(bar(kDrain), 0) || now_ns() > t_end) break;
-            }
+            __syncwarp();
+            if (++st == L.stages) st = 0, ph ^= 1;
+        }
+        if (*abort_flag && lane == 0) {  // tensor memory is given back only when nothing writes to it
+            const uint64_t t_end = now_ns() + 2000000000ull;
+            mma_commit(bar(kDrain));
+            for (uint32_t it = 0; it < kSpinLimit; ++it)
+                if (try_wait(bar(kDrain), 0) || now_ns() > t_end) break;
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ step sizes and decays
+        const int first = warp - (kWarps + 2);
         double seg_log[HP];
+        float A[HP], bias[HP];
+        uint32_t raw_dt[HP][2];  // the step inputs of this warp's next chunk, loaded a chunk ahead
+        const __nv_bfloat16* dt = reinterpret_cast<const __nv_bfloat16*>(p.dt) + b * p.dts.b + (g * hg + head0) * p.dts.h;
+        auto fetch = [&](int c) {
 #pragma unroll
-        for (int h = 0; h < HP; ++h) seg_log[h] = 0.0;
-        for (int c = 0; c < nch; ++c) {
+            for (int h = 0; h < HP; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int t = r.first + c * kQ + 2 * lane + k;
+                    raw_dt[h][k] = (head0 + h < hg && t < r.last) ? __bfloat16_as_ushort(dt[t * p.dts.t + h * p.dts.h]) : 0u;
+                }
+        };
+#pragma unroll
+        for (int h = 0; h < HP; ++h) {
+            const bool real = head0 + h < hg;
+            seg_log[h] = 0.0;
+            A[h] = real ? p.A[g * hg + head0 + h] : 0.0f;
+            bias[h] = (real && p.dt_bias) ? p.dt_bias[g * hg + head0 + h] : 0.0f;
+        }
+        if (first < nch) fetch(first);
+        for (int c = first; c < nch; c += kDtWarps) {
             const int st = c % L.stages;
             if (c >= L.stages) wait(kEmpty + st, ((c / L.stages) - 1) & 1);
             if (*abort_flag) break;
             const int t0 = r.first + c * kQ;
+            float d[HP][2];
+#pragma unroll
+            for (int h = 0; h < HP; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)  // a token that is not there neither decays nor writes
+                    d[h][k] = (head0 + h < hg && t0 + 2 * lane + k < r.last)
+                                  ? step_size(__uint_as_float(raw_dt[h][k] << 16), bias[h], p.softplus, p.dt_min, p.dt_max)
+                                  : 0.0f;
+            if (c + kDtWarps < nch) fetch(c + kDtWarps);
 #pragma unroll
             for (int h = 0; h < HP; ++h) {
-                const int hl = head0 + h, hh = g * hg + hl;
-                const bool real = hl < hg;
-                const float A = real ? p.A[hh] : 0.0f, bias = (real && p.dt_bias) ? p.dt_bias[hh] : 0.0f;
-                float d[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int t = t0 + 2 * lane + k;
-                    d[k] = 0.0f;  // a token that is not there neither decays nor writes
-                    if (real && t < r.last)
-                        d[k] = step_size(load_in(p.dt, static_cast<size_t>(b * p.dts.b + t * p.dts.t + hh * p.dts.h), 1), bias, p.softplus,
-                                         p.dt_min, p.dt_max);
-                }
-                const double a0 = static_cast<double>(d[0]) * A, a1 = static_cast<double>(d[1]) * A;
+                const double a0 = static_cast<double>(d[h][0]) * A[h], a1 = static_cast<double>(d[h][1]) * A[h];
                 double sum = a0 + a1;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -479,15 +512,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     const double cum = k ? sum : sum - a1;
                     const double l2 = cum * 1.4426950408889634074;
                     const float hi = static_cast<float>(l2), lo = static_cast<float>(l2 - static_cast<double>(hi));
-                    const float w = d[k] * expf(static_cast<float>(total - cum));
+                    const float w = d[h][k] * expf(static_cast<float>(total - cum));
                     const int j = 2 * lane + k;
-                    tk.t[j] = make_float4(hi, lo, d[k], w);
+                    tk.t[j] = make_float4(hi, lo, d[h][k], w);
                     tk.hi[j] = hi;
                     tk.lo[j] = lo;
                     tk.ein[j] = expf(static_cast<float>(cum));
                     tk.w[j] = w;
                 }
-                if (lane == 0) tk.dec = static_cast<float>(exp(total));
+                const float dec = static_cast<float>(exp(total));
+                if (lane == 0) tk.dec = dec;
                 seg_log[h] += total;
             }
             __syncwarp();
@@ -495,15 +529,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         }
         if (!OUT && lane == 0) {
 #pragma unroll
-            for (int h = 0; h < HP; ++h)
-                if (head0 + h < hg && c0 % p.P == 0)
-                    p.seg_decay[(static_cast<int64_t>(b) * p.H + g * hg + head0 + h) * p.nseg + seg] = static_cast<float>(exp(seg_log[h]));
+            for (int h = 0; h < HP; ++h) log_mem[first][h] = seg_log[h];
         }
     }
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
     if (warp == kWarps) tmem_dealloc(tm, 512);
+    if (!OUT && threadIdx.x < HP && head0 + static_cast<int>(threadIdx.x) < hg && c0 % p.P == 0) {
+        double sum = 0.0;
+        for (int k = 0; k < kDtWarps; ++k) sum += log_mem[k][threadIdx.x];
+        p.seg_decay[(static_cast<int64_t>(b) * p.H + g * hg + head0 + threadIdx.x) * p.split.pieces() + seg] = static_cast<float>(exp(sum));
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -563,12 +600,12 @@ template <int N, int HP>
 cudaError_t all(const SsmParams& p, const MmaMaps& m, cudaStream_t s)
 {
     const int tiles = (p.H / p.G * p.P + 127) / 128;
-    if (p.nseg > 1) {
-        cudaError_t e = go<N, HP, false>(p, m, tiles, p.nseg - 1, s);
+    if (p.split.nseg > 1) {
+        cudaError_t e = go<N, HP, false>(p, m, tiles, p.split.pieces(), s);
         if (e == cudaSuccess) e = launch_ssm_chain(p, s);
         if (e != cudaSuccess) return e;
     }
-    return go<N, HP, true>(p, m, tiles, p.nseg, s);
+    return go<N, HP, true>(p, m, tiles, p.split.nseg, s);
 }
 
 template <int N>
