@@ -31,18 +31,16 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-// The long part of a wait: at most kSpinLimit polls and limit_ns.  On expiry the status word gets
-// kDevTimeout and the block's abort flag is raised, after which every wait returns at once.
-__device__ __noinline__ void wait_long(uint32_t bar, uint32_t parity, uint32_t* status, volatile int* abort_flag, uint64_t limit_ns)
+// Bounded wait for phase `parity`: at most limit_ns, after which the block's abort flag is raised and
+// every wait returns at once (the kernel reports the flag in the status word at its end).  Short,
+// because it is inlined at every hand-over and the roles of a block compete for the instruction cache.
+__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns)
 {
-    const uint64_t t_end = now_ns() + limit_ns;
-    for (uint32_t it = 0; it < kSpinLimit; ++it) {
-        if (*abort_flag) return;
-        if (try_wait(bar, parity)) return;
-        if (now_ns() > t_end) break;
-    }
-    *abort_flag = 1;
-    set_status(status, kDevTimeout);
+    if (try_wait(bar, parity)) return;
+    const uint64_t t0 = now_ns();
+#pragma unroll 1
+    while (!try_wait(bar, parity) && !*abort_flag)
+        if (now_ns() - t0 > limit_ns) *abort_flag = 1;
 }
 
 __device__ __forceinline__ void arrive(uint32_t bar)
@@ -112,17 +110,6 @@ __device__ __forceinline__ void mma_ss(uint32_t d, Desc a, Desc b, uint32_t word
         : "memory");
 }
 
-// ... leaving alone the tensor-memory lanes whose bit is set in m0 (lanes 0..31) .. m3 (96..127)
-__device__ __forceinline__ void mma_ss_masked(uint32_t d, Desc a, Desc b, uint32_t word, uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3,
-                                              bool add)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, {%7, %8, %9, %10}, p;\n\t}" ::"r"(d),
-        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(m0), "r"(m1), "r"(m2), "r"(m3)
-        : "memory");
-}
-
 // first operand in tensor memory (two bf16 along the contraction per 32-bit column)
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t word, bool add)
 {
@@ -130,6 +117,17 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t 
         "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
         "r"(a), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+// ... leaving alone the tensor-memory lanes whose bit is set in m0 (lanes 0..31) .. m3 (96..127)
+__device__ __forceinline__ void mma_ts_masked(uint32_t d, uint32_t a, Desc b, uint32_t word, uint32_t m0, uint32_t m1, uint32_t m2,
+                                              uint32_t m3, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, {%6, %7, %8, %9}, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(m0), "r"(m1), "r"(m2), "r"(m3)
         : "memory");
 }
 
@@ -213,6 +211,18 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t a, const uint32_t (&v)[N])
     }
 }
 
+// Registers per thread of the calling warpgroup from here on.
+template <int N>
+__device__ __forceinline__ void regs_up()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ------------------------------------------------------------------ shared-memory fragments
 
 // Four 8x8 blocks of 16-bit values, transposed: lane t gets, of block k, rows 2 (t%4) and +1 of
@@ -230,24 +240,64 @@ __device__ __forceinline__ void stsm_t(uint32_t addr, uint32_t v0, uint32_t v1, 
                  : "memory");
 }
 
+// ------------------------------------------------------------------ pairs of fp32 in one instruction
+
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void un(F2 p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // ------------------------------------------------------------------ values as bf16 pieces
 
 __device__ __forceinline__ float bf_lo(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
+__device__ __forceinline__ F2 bf_pair(uint32_t pair) { return f2(bf_lo(pair), bf_hi(pair)); }
 
-__device__ __forceinline__ uint32_t pack_rn(float a, float b)  // a in the low half
+__device__ __forceinline__ uint32_t pack_rn(F2 p)  // the first value in the low half
 {
+    float a, b;
+    un(p, a, b);
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-
-// The leading 8 bits of a and b as one pair, and what is left of them.
-__device__ __forceinline__ uint32_t peel(float& a, float& b)
+__device__ __forceinline__ uint32_t pack_cut(F2 p)  // the leading 8 bits of both
 {
+    float a, b;
+    un(p, a, b);
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+// The leading 8 bits of both as one pair of bf16; p keeps what is left (exact).
+__device__ __forceinline__ uint32_t peel(F2& p)
+{
+    float a, b;
+    un(p, a, b);
     const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    a -= __uint_as_float(ua & 0xffff0000u);
-    b -= __uint_as_float(ub & 0xffff0000u);
+    p = add2(p, f2(__uint_as_float((ua & 0xffff0000u) ^ 0x80000000u), __uint_as_float((ub & 0xffff0000u) ^ 0x80000000u)));
     return __byte_perm(ua, ub, 0x7632);
 }
 

@@ -33,8 +33,12 @@
 namespace ramnet {
 namespace {
 
+// Registers per thread by role: 20 warps launch with 96 each, and 2 x 80 + 2 x 128 + 64 = 5 x 96.
+constexpr int kInRegs = 80, kOutRegs = 128, kMiscRegs = 64;
 constexpr int kQ = 64;           // tokens per chunk
-constexpr int kWarps = 16;       // elementwise warps
+constexpr int kInWarps = 8;      // warps that prepare operands (W, Xw)
+constexpr int kOutWarps = 8;     // warps that hold the state and write y
+constexpr int kWarps = kInWarps + kOutWarps;
 constexpr int kDtWarps = 2;      // warps that compute step sizes and decays, in alternate chunks
 constexpr int kThreads = (kWarps + 2 + kDtWarps) * 32;
 constexpr int kStgPitch = 80;    // bytes per token row of a warp's y patch: 64 used; conflict-free
@@ -49,7 +53,7 @@ struct Tok {
     float dec, pad[3];     // exp(a_63)
 };
 
-enum Bar { kLanded = 0, kToks = 4, kEmpty = 8, kFixed = 12, kG, kW, kY, kYfree, kS, kXw, kDs = kXw + 2, kDrain = kDs + 2, kBars };
+enum Bar { kLanded = 0, kToks = 4, kEmpty = 8, kFixed = 12, kG, kW, kY, kYfree, kS, kXw, kDs = kXw + 2, kDsFree = kDs + 2, kDrain = kDsFree + 2, kBars };
 
 struct Layout {
     int stages;
@@ -63,12 +67,12 @@ __host__ __device__ constexpr Layout layout_of(int N, int HP, bool out)
     l.b_off = 16384;
     l.c_off = l.b_off + nt;
     l.stage_bytes = l.c_off + (out ? nt : 0);
-    const uint32_t fixed = (out ? HP * 16384u + kWarps * 16 * kStgPitch : 0);
+    const uint32_t fixed = (out ? HP * 16384u + kOutWarps * 32 * kStgPitch : 0);
     l.stages = 4;
     while (l.stages > 2 && l.stages * (l.stage_bytes + HP * sizeof(Tok)) + fixed + 1024 > kSmemMax) --l.stages;
     l.w_off = l.stages * l.stage_bytes;
     l.stg_off = l.w_off + (out ? HP * 16384u : 0);
-    l.tok_off = l.stg_off + (out ? kWarps * 16 * kStgPitch : 0);
+    l.tok_off = l.stg_off + (out ? kOutWarps * 32 * kStgPitch : 0);
     l.total = l.tok_off + l.stages * HP * static_cast<uint32_t>(sizeof(Tok)) + 1024;  // 1024: base alignment
     return l;
 }
@@ -91,7 +95,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
 {
     constexpr Layout L = layout_of(N, HP, OUT);
     constexpr int NB = OUT ? 1 : 2;  // buffers of Xw and dS
-    constexpr uint32_t cDs = 0, cShi = N, cSlo = N + N / 2, cXw = 256, cYb = 352, cYa = 416;  // tensor-memory columns
+    // tensor-memory columns (G shares those of Ya; without outputs dS and Xw have two buffers)
+    constexpr uint32_t cDs = 0, cShi = 128, cSlo = 192, cXw = 256, cX = 352, cYb = 384, cYa = 448;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bar_mem[kBars];
     __shared__ uint32_t tmem_holder;
@@ -114,25 +119,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
 
     auto bar = [&](int i) { return bars + 8u * i; };
     auto wait = [&](int i, uint32_t parity) {
-        if (!try_wait(bars + 8u * i, parity)) wait_long(bars + 8u * i, parity, p.status, abort_flag, p.wait_ns);
+        wait_phase(bars + 8u * i, parity, abort_flag, p.wait_ns);
     };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(bar_mem + kLanded + i, 1);
             mbar_init(bar_mem + kToks + i, 1);
-            mbar_init(bar_mem + kEmpty + i, kWarps);
+            mbar_init(bar_mem + kEmpty + i, kOutWarps);
         }
         mbar_init(bar_mem + kFixed, 1);
         mbar_init(bar_mem + kG, 1);
         mbar_init(bar_mem + kDrain, 1);
-        mbar_init(bar_mem + kW, kWarps);
+        mbar_init(bar_mem + kW, kInWarps);
         mbar_init(bar_mem + kY, 1);
-        mbar_init(bar_mem + kYfree, kWarps);
-        mbar_init(bar_mem + kS, kWarps);
+        mbar_init(bar_mem + kYfree, kOutWarps);
+        mbar_init(bar_mem + kS, kOutWarps);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar_mem + kXw + i, kWarps);
+            mbar_init(bar_mem + kXw + i, kInWarps);
             mbar_init(bar_mem + kDs + i, 1);
+            mbar_init(bar_mem + kDsFree + i, kOutWarps);
         }
         abort_mem = 0;
         fence_mbar_init_cluster();
@@ -148,205 +154,258 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     tmem_fence_after_sync();
     const uint32_t tm = tmem_holder;
 
-    if (warp < kWarps) {
-        // ------------------------------------------------------------ elementwise warps
-        const int q = warp & 3, cb = warp >> 2;
-        const uint32_t tq = tm + (static_cast<uint32_t>(q) << 21);  // this warp's 32 lanes
-        const int hw = HP == 4 ? q : HP == 2 ? q >> 1 : 0;          // head of its channels
-        const int ch = c0 + q * 32 + lane;                          // channel of state column work
+    const int q = warp & 3, part = (warp >> 2) & 1;                  // tensor-memory quadrant; half of the tokens or state columns
+    const uint32_t tq = tm + (static_cast<uint32_t>(q) << 21);      // this warp's 32 lanes
+    const int hw = HP == 4 ? q : HP == 2 ? q >> 1 : 0;              // head of its channels
+    // ldmatrix row of this lane in a block of 16 tokens x 16 channels (and stmatrix row in a patch of y)
+    const int row = 8 * (lane >> 4) + (lane & 7), pcol = 8 * ((lane >> 3) & 1);
+    uint32_t xaddr[2];  // channels q*32 + half*16.., tokens part*32..
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int pp = q * 32 + half * 16 + pcol;
+        xaddr[half] = s0 + (pp >> 6) * 8192 + (part * 32 + row) * 128 + ((((pp & 63) >> 3) ^ (row & 7)) << 4);
+    }
+    auto done = [&](int i) {  // this warp's part of hand-over i
+        tmem_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(bar(i));
+    };
+
+    if (warp < kInWarps) {
+        // ------------------------------------------------------------ operands of the chunk: Xw, X^T and W
+        regs_down<kInRegs>();
+        int st = 0;
+        uint32_t ph = 0;
+        for (int c = 0; c < nch; ++c) {
+            const Tok* tok = toks + st * HP;
+            wait(kToks + st, ph);
+            wait(kLanded + st, ph);
+            if (r.last - r.first - c * kQ < kQ) wait(kFixed, 0);
+            const int i = NB == 2 ? c & 1 : 0;
+            // Xw's buffer: the product that read it is done
+            if (c >= NB) wait(kDs + i, NB == 2 ? ((c >> 1) - 1) & 1 : (c - 1) & 1);
+            tmem_fence_after_sync();
+#pragma unroll 1
+            for (int tg = 0; tg < 2; ++tg) {
+                const uint32_t xw = tq + cXw + i * 96 + part * 16 + tg * 8;
+                const float* w = tok[hw].w + part * 32 + tg * 16 + 2 * (lane & 3);
+                const float2 w0 = *reinterpret_cast<const float2*>(w), w1 = *reinterpret_cast<const float2*>(w + 8);
+                const F2 ww[2] = {f2(w0.x, w0.y), f2(w1.x, w1.y)};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t xx[4];
+                    ldsm_t(xaddr[half] + st * L.stage_bytes + tg * 2048, xx);
+                    uint32_t piece[3][4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        F2 v = mul2(bf_pair(xx[k]), ww[k >> 1]);
+                        piece[0][k] = peel(v);
+                        piece[1][k] = peel(v);
+                        piece[2][k] = pack_cut(v);
+                    }
+#pragma unroll
+                    for (int s = 0; s < 3; ++s)
+                        tmem_st_16x8(xw + (static_cast<uint32_t>(half) << 20) + s * 32, piece[s][0], piece[s][1], piece[s][2], piece[s][3]);
+                }
+            }
+            tmem_wait_st();
+            done(kXw + i);
+            if constexpr (OUT) {
+                if (c > 0) wait(kY, (c - 1) & 1);  // X^T's buffer
+                tmem_fence_after_sync();
+#pragma unroll 1
+                for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t xx[4];
+                        ldsm_t(xaddr[half] + st * L.stage_bytes + tg * 2048, xx);
+                        tmem_st_16x8(tq + (static_cast<uint32_t>(half) << 20) + cX + part * 16 + tg * 8, xx[0], xx[1], xx[2], xx[3]);
+                    }
+                wait(kG, c & 1);
+                tmem_fence_after_sync();
+                // tokens j of block q reach tokens i of blocks q..3; this warp takes every second of them
+#pragma unroll 1
+                for (int cb = q + part; cb < 4; cb += 2) {
+                    float gv[8];
+                    tmem_ld_16x16(tq + cYa + cb * 16, gv);
+                    const int j = q * 16 + (lane >> 2), i0 = cb * 16 + 2 * (lane & 3);
+                    tmem_wait_ld();
+                    settle(gv);
+#pragma unroll
+                    for (int h = 0; h < HP; ++h) {
+                        const Tok& tk = tok[h];
+                        const uint32_t wbase = L.w_off + h * 16384 + j * 128 + (i0 & 7) * 2;
+                        F2 hi[2], lo[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float2 a = *reinterpret_cast<const float2*>(tk.hi + i0 + 8 * k);
+                            const float2 e = *reinterpret_cast<const float2*>(tk.lo + i0 + 8 * k);
+                            hi[k] = f2(a.x, a.y);
+                            lo[k] = f2(e.x, e.y);
+                        }
+#pragma unroll
+                        for (int rb = 0; rb < 2; ++rb) {
+                            const float4 tj = tk.t[j + 8 * rb];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float u, v;
+                                un(add2(add2(hi[k], f2(-tj.x, -tj.x)), add2(lo[k], f2(-tj.y, -tj.y))), u, v);
+                                const F2 e = mul2(f2(ex2(u), ex2(v)), f2(tj.z, tj.z));
+                                F2 w = mul2(e, f2(gv[4 * k + 2 * rb], gv[4 * k + 2 * rb + 1]));
+                                if (cb == q) {
+                                    const int ii = i0 + 8 * k - (j + 8 * rb);
+                                    un(w, u, v);
+                                    w = f2(ii >= 0 ? u : 0.0f, ii >= -1 ? v : 0.0f);
+                                }
+                                const uint32_t at = wbase + rb * 1024 + ((((i0 >> 3) + k) ^ (j & 7)) << 4);
+                                *reinterpret_cast<uint32_t*>(sm + at) = peel(w);
+                                *reinterpret_cast<uint32_t*>(sm + at + 8192) = pack_rn(w);
+                            }
+                        }
+                    }
+                }
+                fence_async_smem();
+                tmem_wait_st();
+                done(kW);
+            }
+            if (++st == L.stages) st = 0, ph ^= 1;
+        }
+    } else if (warp < kWarps) {
+        // ------------------------------------------------------------ state and outputs
+        regs_up<kOutRegs>();
+        const int ch = c0 + q * 32 + lane;  // channel of this lane's state columns
         const bool mine = ch < cend;
         const int64_t bh = static_cast<int64_t>(b) * p.H + g * hg + ch / p.P;
         const int64_t np = static_cast<int64_t>(N) * p.P;
         const int pc = ch % p.P;
         const float skip = (OUT && p.D && mine) ? p.D[g * hg + (c0 + q * 32) / p.P] : 0.0f;
-        constexpr int NC = N / 4;  // state columns per warp
-        float S[NC];
+        const F2 skip2 = f2(skip, skip);
+        constexpr int NC = N / 2;            // state columns per warp
+        constexpr int NV = NC < 16 ? NC : 16;  // of them per tensor-memory access
+        F2 S[NC / 2];
         {
             const float* from = nullptr;
             if (OUT && mine) {
                 if (p.split.nseg > 1) from = p.seg_state + (bh * p.split.slots() + seg * p.split.sub) * np;
                 else if (p.S_in) from = p.S_in + bh * np;
             }
-#pragma unroll
-            for (int k = 0; k < NC; ++k) S[k] = from ? from[static_cast<int64_t>(cb * NC + k) * p.P + pc] : 0.0f;
-        }
-        auto put_state = [&]() {
-            uint32_t hi[NC / 2], lo[NC / 2];
+            from = from ? from + static_cast<int64_t>(part) * NC * p.P + pc : nullptr;
 #pragma unroll
             for (int k = 0; k < NC / 2; ++k) {
-                float u = S[2 * k], v = S[2 * k + 1];
-                hi[k] = peel(u, v);
-                lo[k] = pack_rn(u, v);
+                S[k] = from ? f2(from[0], from[p.P]) : f2(0.0f, 0.0f);
+                if (from) from += 2 * p.P;
+                if (k % 8 == 7) asm volatile("" ::: "memory");  // few loads, and few addresses, at a time
             }
-            tmem_st_cols<NC / 2>(tq + cShi + cb * (NC / 2), hi);
-            tmem_st_cols<NC / 2>(tq + cSlo + cb * (NC / 2), lo);
-            tmem_wait_st();
-        };
-        auto done = [&](int i) {  // this warp's part of hand-over i
-            tmem_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) arrive(bar(i));
+        }
+        auto put_state = [&](int k0) {  // state columns k0 .. k0+NV as two pieces
+            uint32_t hi[NV / 2], lo[NV / 2];
+#pragma unroll
+            for (int k = 0; k < NV / 2; ++k) {
+                F2 v = S[k0 / 2 + k];
+                hi[k] = peel(v);
+                lo[k] = pack_rn(v);
+            }
+            tmem_st_cols<NV / 2>(tq + cShi + (part * NC + k0) / 2, hi);
+            tmem_st_cols<NV / 2>(tq + cSlo + (part * NC + k0) / 2, lo);
         };
         if (OUT && nch > 0) {
-            put_state();
+#pragma unroll
+            for (int k0 = 0; k0 < NC; k0 += NV) put_state(k0);
+            tmem_wait_st();
             done(kS);
         }
-        // ldmatrix row of this lane: token cb*16 + row, 8 channels; and of the y patch
-        const int row = 8 * (lane >> 4) + (lane & 7), pcol = 8 * ((lane >> 3) & 1);
-        const int jrow = cb * 16 + row;
-        uint32_t xaddr[2];
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int pp = q * 32 + half * 16 + pcol;
-            xaddr[half] = s0 + (pp >> 6) * 8192 + jrow * 128 + ((((pp & 63) >> 3) ^ (jrow & 7)) << 4);
-        }
-        const uint32_t patch = s0 + L.stg_off + warp * 16 * kStgPitch;
-        auto sum_state = [&](int c, const Tok* tok) {  // S' = dec S + dS
-            const int i = NB == 2 ? c & 1 : 0;
-            wait(kDs + i, NB == 2 ? (c >> 1) & 1 : c & 1);
-            tmem_fence_after_sync();
-            float d[NC];
-            tmem_ld_cols<NC>(tq + cDs + i * N + cb * NC, d);
-            const float dec = tok[hw].dec;
-            tmem_wait_ld();
-            settle(d);
-#pragma unroll
-            for (int k = 0; k < NC; ++k) S[k] = fmaf(S[k], dec, d[k]);
-        };
-        // this lane's 16 bytes of y: token cb*16 + lane/4 (+8), 8 channels
-        const int ycol = c0 + q * 32 + (lane & 3) * 8, ytok = cb * 16 + (lane >> 2);
+        // this lane's 16 bytes of y: token part*32 + lane/4 (+8..), 8 channels
+        const uint32_t patch = L.stg_off + (warp - kInWarps) * 32 * kStgPitch;
+        const int ycol = c0 + q * 32 + (lane & 3) * 8, ytok = part * 32 + (lane >> 2);
         const int64_t yrow = static_cast<int64_t>(p.H) * p.P;
         __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.T + r.first + ytok) * yrow + g * cend + ycol;
         int st = 0;
         uint32_t ph = 0;
         for (int c = 0; c < nch; ++c) {
-            const int nv = min(kQ, r.last - r.first - c * kQ);
-            const Tok* tok = toks + st * HP;
+            const Tok& tok = toks[st * HP + hw];
             wait(kToks + st, ph);
-            wait(kLanded + st, ph);
-            if (nv < kQ) wait(kFixed, 0);
             if constexpr (OUT) {
-                wait(kG, c & 1);
-                tmem_fence_after_sync();
-                if (cb >= q) {  // tokens j of block q reach tokens i of block cb
-                    float gv[8];
-                    tmem_ld_16x16(tq + cYa + cb * 16, gv);
-                    const int j = q * 16 + (lane >> 2), i = cb * 16 + 2 * (lane & 3);
-                    tmem_wait_ld();
-                    settle(gv);
-#pragma unroll
-                    for (int h = 0; h < HP; ++h) {
-                        const Tok& tk = tok[h];
-                        const uint32_t wbase = L.w_off + h * 16384;
-#pragma unroll
-                        for (int rb = 0; rb < 2; ++rb) {
-                            const float4 tj = tk.t[j + 8 * rb];
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                const int ii = i + 8 * k;
-                                const float2 hi = *reinterpret_cast<const float2*>(tk.hi + ii);
-                                const float2 lo = *reinterpret_cast<const float2*>(tk.lo + ii);
-                                float u = gv[4 * k + 2 * rb] * (tj.z * ex2((hi.x - tj.x) + (lo.x - tj.y)));
-                                float v = gv[4 * k + 2 * rb + 1] * (tj.z * ex2((hi.y - tj.x) + (lo.y - tj.y)));
-                                if (cb == q) {
-                                    u = ii >= j + 8 * rb ? u : 0.0f;
-                                    v = ii + 1 >= j + 8 * rb ? v : 0.0f;
-                                }
-                                const uint32_t at = wbase + (j + 8 * rb) * 128 + ((((ii >> 3)) ^ (j & 7)) << 4) + (ii & 7) * 2;
-                                const uint32_t wh = peel(u, v);
-                                *reinterpret_cast<uint32_t*>(sm + at) = wh;
-                                *reinterpret_cast<uint32_t*>(sm + at + 8192) = pack_rn(u, v);
-                            }
-                        }
-                    }
-                    fence_async_smem();
-                }
-                done(kW);
-            }
-            // Xw: this warp's 32 channels x 16 tokens, three exact pieces
-            uint32_t x[2][4];
-            {
-                const uint32_t xw = tq + cXw + (NB == 2 ? (c & 1) * 96 : 0) + cb * 8;
-                const float* w = tok[hw].w + cb * 16 + 2 * (lane & 3);
-                const float2 w0 = *reinterpret_cast<const float2*>(w), w1 = *reinterpret_cast<const float2*>(w + 8);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    ldsm_t(xaddr[half] + st * L.stage_bytes, x[half]);
-                    uint32_t piece[3][4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 ww = k < 2 ? w0 : w1;
-                        float u = bf_lo(x[half][k]) * ww.x, v = bf_hi(x[half][k]) * ww.y;
-                        piece[0][k] = peel(u, v);
-                        piece[1][k] = peel(u, v);
-                        piece[2][k] = __byte_perm(__float_as_uint(u), __float_as_uint(v), 0x7632);
-                    }
-#pragma unroll
-                    for (int s = 0; s < 3; ++s)
-                        tmem_st_16x8(xw + (static_cast<uint32_t>(half) << 20) + s * 32, piece[s][0], piece[s][1], piece[s][2], piece[s][3]);
-                }
-                tmem_wait_st();
-                done(kXw + (NB == 2 ? c & 1 : 0));
-            }
-            if constexpr (OUT) {
-                // y of this warp's 32 channels x 16 tokens
-                const float* e = tok[hw].ein + cb * 16 + 2 * (lane & 3);
-                const float2 e0 = *reinterpret_cast<const float2*>(e), e1 = *reinterpret_cast<const float2*>(e + 8);
+                wait(kLanded + st, ph);
                 wait(kY, c & 1);
                 tmem_fence_after_sync();
+                // y of 32 channels x 32 tokens, through registers into this warp's patch
+#pragma unroll 1
+                for (int tg = 0; tg < 2; ++tg) {
+                    float yb[2][8], ya[2][8];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float yb[8], ya[8];
-                    tmem_ld_16x16(tq + (static_cast<uint32_t>(half) << 20) + cYb + cb * 16, yb);
-                    tmem_ld_16x16(tq + (static_cast<uint32_t>(half) << 20) + cYa + cb * 16, ya);
-                    tmem_wait_ld();
-                    settle(yb);
-                    settle(ya);
-                    uint32_t o[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // 8 tokens k/2, 8 channels k%2
-                        const int at = 4 * (k >> 1) + 2 * (k & 1);
-                        const float2 ee = k < 2 ? e0 : e1;
-                        const float u = fmaf(skip, bf_lo(x[half][k]), fmaf(ee.x, yb[at], ya[at]));
-                        const float v = fmaf(skip, bf_hi(x[half][k]), fmaf(ee.y, yb[at + 1], ya[at + 1]));
-                        o[k] = pack_rn(u, v);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t at = tq + (static_cast<uint32_t>(half) << 20) + part * 32 + tg * 16;
+                        tmem_ld_16x16(at + cYb, yb[half]);
+                        tmem_ld_16x16(at + cYa, ya[half]);
                     }
-                    stsm_t(patch + row * kStgPitch + (half * 16 + pcol) * 2, o[0], o[1], o[2], o[3]);
+                    const float* e = tok.ein + part * 32 + tg * 16 + 2 * (lane & 3);
+                    const float2 e0 = *reinterpret_cast<const float2*>(e), e1 = *reinterpret_cast<const float2*>(e + 8);
+                    const F2 ee[2] = {f2(e0.x, e0.y), f2(e1.x, e1.y)};
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        settle(yb[half]);
+                        settle(ya[half]);
+                        uint32_t xx[4], o[4];
+                        ldsm_t(xaddr[half] + st * L.stage_bytes + tg * 2048, xx);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {  // 8 tokens k/2, 8 channels k%2
+                            const int at = 4 * (k >> 1) + 2 * (k & 1);
+                            const F2 v = fma2(ee[k >> 1], f2(yb[half][at], yb[half][at + 1]), f2(ya[half][at], ya[half][at + 1]));
+                            o[k] = pack_rn(fma2(skip2, bf_pair(xx[k]), v));
+                        }
+                        stsm_t(s0 + patch + (tg * 16 + row) * kStgPitch + (half * 16 + pcol) * 2, o[0], o[1], o[2], o[3]);
+                    }
                 }
                 done(kYfree);
+                const int nv = min(kQ, r.last - r.first - c * kQ);
 #pragma unroll
-                for (int it = 0; it < 2; ++it) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(sm + L.stg_off + (warp * 16 + (lane >> 2) + 8 * it) * kStgPitch + (lane & 3) * 16);
+                for (int it = 0; it < 4; ++it) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(sm + patch + ((lane >> 2) + 8 * it) * kStgPitch + (lane & 3) * 16);
                     if (ytok + 8 * it < nv && ycol < cend) *reinterpret_cast<uint4*>(yp + it * 8 * yrow) = v;
                 }
                 yp += kQ * yrow;
-                sum_state(c, tok);
-                if (c + 1 < nch) {
-                    put_state();
-                    done(kS);
-                }
-                __syncwarp();
-                if (lane == 0) arrive(bar(kEmpty + st));
-            } else if (c > 0) {
-                const int before = st == 0 ? L.stages - 1 : st - 1;
-                sum_state(c - 1, toks + before * HP);
-                __syncwarp();
-                if (lane == 0) arrive(bar(kEmpty + before));
             }
+            // S' = dec S + dS
+            const int i = NB == 2 ? c & 1 : 0;
+            wait(kDs + i, NB == 2 ? (c >> 1) & 1 : c & 1);
+            tmem_fence_after_sync();
+            const F2 dec = f2(tok.dec, tok.dec);
+#pragma unroll
+            for (int k0 = 0; k0 < NC; k0 += NV) {
+                float d[NV];
+                tmem_ld_cols<NV>(tq + cDs + i * 128 + part * NC + k0, d);
+                tmem_wait_ld();
+                settle(d);
+#pragma unroll
+                for (int k = 0; k < NV / 2; ++k) S[k0 / 2 + k] = fma2(S[k0 / 2 + k], dec, f2(d[2 * k], d[2 * k + 1]));
+                if (k0 + NV == NC) done(kDsFree + i);
+                if (OUT && c + 1 < nch) put_state(k0);
+            }
+            if (OUT && c + 1 < nch) {
+                tmem_wait_st();
+                done(kS);
+            }
+            __syncwarp();
+            if (lane == 0) arrive(bar(kEmpty + st));
             if (++st == L.stages) st = 0, ph ^= 1;
         }
-        if (!OUT && nch > 0) sum_state(nch - 1, toks + (st == 0 ? L.stages - 1 : st - 1) * HP);
         float* to = nullptr;
         if (mine) {
             if (!OUT) to = p.seg_state + (bh * p.split.slots() + seg) * np;
             else if (seg == p.split.nseg - 1) to = p.S_out + bh * np;
         }
         if (to) {
+            to += static_cast<int64_t>(part) * NC * p.P + pc;
 #pragma unroll
-            for (int k = 0; k < NC; ++k) to[static_cast<int64_t>(cb * NC + k) * p.P + pc] = S[k];
+            for (int k = 0; k < NC / 2; ++k) {
+                un(S[k], to[0], to[p.P]);
+                to += 2 * p.P;
+            }
         }
     } else if (warp == kWarps) {
         // ------------------------------------------------------------ TMA
+        regs_down<kMiscRegs>();
         int issued = 0;
         for (int c = 0; c < nch; ++c) {
             const int st = c % L.stages;
@@ -384,8 +443,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         }
     } else if (warp == kWarps + 1) {
         // ------------------------------------------------------------ MMA issue (whole warp, one lane issues)
+        regs_down<kMiscRegs>();
         constexpr uint32_t wG = mma_word(64, 64, false, false), wYb = mma_word(128, 64, false, false);
-        constexpr uint32_t wYa = mma_word(128, 64, true, true), wDs = mma_word(128, N, false, true);
+        constexpr uint32_t wYa = mma_word(128, 64, false, true), wDs = mma_word(128, N, false, true);
         const Desc wdesc = desc_of(s0 + L.w_off, 8192);
         int st = 0;
         uint32_t ph = 0;
@@ -406,6 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     mma_commit(bar(kG));
                 }
                 __syncwarp();
+            }
+            if constexpr (OUT) {
                 wait(kS, c & 1);
                 tmem_fence_after_sync();
                 if (elect_one()) {
@@ -425,12 +487,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                         for (int s = 0; s < 2; ++s)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const Desc da = down + k * 2048, db = wdesc + (h * 16384 + (s ? 0 : 8192) + k * 2048);
+                                const Desc db = wdesc + (h * 16384 + (s ? 0 : 8192) + k * 2048);
                                 if constexpr (HP == 1) {
-                                    mma_ss(tm + cYa, da, db, wYa, s + k > 0);
+                                    mma_ts(tm + cYa, tm + cX + k * 8, db, wYa, s + k > 0);
                                 } else {
                                     auto off = [&](int qq) { return (HP == 4 ? qq : qq >> 1) == h ? 0u : 0xffffffffu; };
-                                    mma_ss_masked(tm + cYa, da, db, wYa, off(0), off(1), off(2), off(3), s + k > 0);
+                                    mma_ts_masked(tm + cYa, tm + cX + k * 8, db, wYa, off(0), off(1), off(2), off(3), s + k > 0);
                                 }
                             }
                     mma_commit(bar(kY));
@@ -439,13 +501,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             }
             const int i = NB == 2 ? c & 1 : 0;
             wait(kXw + i, NB == 2 ? (c >> 1) & 1 : c & 1);
+            if (c >= NB) wait(kDsFree + i, NB == 2 ? ((c >> 1) - 1) & 1 : (c - 1) & 1);
             tmem_fence_after_sync();
             if (elect_one()) {
 #pragma unroll
-                for (int s = 2; s >= 0; --s)
+                for (int s = 2; s >= 0; --s)  // the small pieces first
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ts(tm + cDs + i * N, tm + cXw + i * 96 + s * 32 + k * 8, down + (L.b_off + k * 2048), wDs, s < 2 || k > 0);
+                        mma_ts(tm + cDs + i * 128, tm + cXw + i * 96 + s * 32 + k * 8, down + (L.b_off + k * 2048), wDs, s < 2 || k > 0);
                 mma_commit(bar(kDs + i));
             }
             __syncwarp();
@@ -460,47 +523,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         __syncwarp();
     } else {
         // ------------------------------------------------------------ step sizes and decays
+        regs_down<kMiscRegs>();
         const int first = warp - (kWarps + 2);
-        double seg_log[HP];
-        float A[HP], bias[HP];
-        uint32_t raw_dt[HP][2];  // the step inputs of this warp's next chunk, loaded a chunk ahead
         const __nv_bfloat16* dt = reinterpret_cast<const __nv_bfloat16*>(p.dt) + b * p.dts.b + (g * hg + head0) * p.dts.h;
-        auto fetch = [&](int c) {
+        if (!OUT && lane < HP) log_mem[first][lane] = 0.0;
+        __syncwarp();
+        uint32_t raw_dt[2];  // the step inputs of the next (chunk, head), loaded one ahead
+        auto fetch = [&](int c, int h) {
 #pragma unroll
-            for (int h = 0; h < HP; ++h)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int t = r.first + c * kQ + 2 * lane + k;
-                    raw_dt[h][k] = (head0 + h < hg && t < r.last) ? __bfloat16_as_ushort(dt[t * p.dts.t + h * p.dts.h]) : 0u;
-                }
+            for (int k = 0; k < 2; ++k) {
+                const int t = r.first + c * kQ + 2 * lane + k;
+                raw_dt[k] = (c < nch && head0 + h < hg && t < r.last) ? __bfloat16_as_ushort(dt[t * p.dts.t + h * p.dts.h]) : 0u;
+            }
         };
-#pragma unroll
-        for (int h = 0; h < HP; ++h) {
-            const bool real = head0 + h < hg;
-            seg_log[h] = 0.0;
-            A[h] = real ? p.A[g * hg + head0 + h] : 0.0f;
-            bias[h] = (real && p.dt_bias) ? p.dt_bias[g * hg + head0 + h] : 0.0f;
-        }
-        if (first < nch) fetch(first);
+        fetch(first, 0);
+#pragma unroll 1
         for (int c = first; c < nch; c += kDtWarps) {
             const int st = c % L.stages;
             if (c >= L.stages) wait(kEmpty + st, ((c / L.stages) - 1) & 1);
             if (*abort_flag) break;
-            const int t0 = r.first + c * kQ;
-            float d[HP][2];
-#pragma unroll
-            for (int h = 0; h < HP; ++h)
+#pragma unroll 1
+            for (int h = 0; h < HP; ++h) {
+                const bool real = head0 + h < hg;
+                const double A = real ? static_cast<double>(p.A[g * hg + head0 + h]) : 0.0;
+                const float bias = (real && p.dt_bias) ? p.dt_bias[g * hg + head0 + h] : 0.0f;
+                float d[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k)  // a token that is not there neither decays nor writes
-                    d[h][k] = (head0 + h < hg && t0 + 2 * lane + k < r.last)
-                                  ? step_size(__uint_as_float(raw_dt[h][k] << 16), bias[h], p.softplus, p.dt_min, p.dt_max)
-                                  : 0.0f;
-            if (c + kDtWarps < nch) fetch(c + kDtWarps);
-#pragma unroll
-            for (int h = 0; h < HP; ++h) {
-                const double a0 = static_cast<double>(d[h][0]) * A[h], a1 = static_cast<double>(d[h][1]) * A[h];
+                    d[k] = (real && r.first + c * kQ + 2 * lane + k < r.last)
+                               ? step_size(__uint_as_float(raw_dt[k] << 16), bias, p.softplus, p.dt_min, p.dt_max)
+                               : 0.0f;
+                if (h + 1 < HP) fetch(c, h + 1);
+                else fetch(c + kDtWarps, 0);
+                const double a0 = d[0] * A, a1 = d[1] * A;
                 double sum = a0 + a1;
-#pragma unroll
+#pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
                     const double up = __shfl_up_sync(0xffffffffu, sum, o);
                     if (lane >= o) sum += up;
@@ -512,30 +569,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     const double cum = k ? sum : sum - a1;
                     const double l2 = cum * 1.4426950408889634074;
                     const float hi = static_cast<float>(l2), lo = static_cast<float>(l2 - static_cast<double>(hi));
-                    const float w = d[h][k] * expf(static_cast<float>(total - cum));
+                    const float w = d[k] * expf(static_cast<float>(total - cum));
                     const int j = 2 * lane + k;
-                    tk.t[j] = make_float4(hi, lo, d[h][k], w);
+                    tk.t[j] = make_float4(hi, lo, d[k], w);
                     tk.hi[j] = hi;
                     tk.lo[j] = lo;
                     tk.ein[j] = expf(static_cast<float>(cum));
                     tk.w[j] = w;
                 }
                 const float dec = static_cast<float>(exp(total));
-                if (lane == 0) tk.dec = dec;
-                seg_log[h] += total;
+                if (lane == 0) {
+                    tk.dec = dec;
+                    if (!OUT) log_mem[first][h] += total;
+                }
             }
             __syncwarp();
             if (lane == 0) arrive(bar(kToks + st));
-        }
-        if (!OUT && lane == 0) {
-#pragma unroll
-            for (int h = 0; h < HP; ++h) log_mem[first][h] = seg_log[h];
         }
     }
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
     if (warp == kWarps) tmem_dealloc(tm, 512);
+    if (threadIdx.x == 0 && *abort_flag) set_status(p.status, kDevTimeout);
     if (!OUT && threadIdx.x < HP && head0 + static_cast<int>(threadIdx.x) < hg && c0 % p.P == 0) {
         double sum = 0.0;
         for (int k = 0; k < kDtWarps; ++k) sum += log_mem[k][threadIdx.x];
@@ -588,6 +644,7 @@ template <int N, int HP, bool OUT>
 cudaError_t go(const SsmParams& p, const MmaMaps& m, int tiles, int segs, cudaStream_t s)
 {
     constexpr Layout L = layout_of(N, HP, OUT);
+    static_assert(kThreads == 640, "register split");
     static_assert(L.total <= kSmemMax, "shared memory");
     auto kern = k_ssm_mma<N, HP, OUT>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L.total));
