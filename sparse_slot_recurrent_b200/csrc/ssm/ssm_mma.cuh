@@ -71,6 +71,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
                  : "memory");
 }
 
+// ... and stores: a box of shared memory out, in this thread's bulk group.  The box may be
+// written again once store_read_done() has returned in the same thread.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int c0, int c1, int c2, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n\tcp.async.bulk.commit_group;" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+__device__ __forceinline__ void store_read_done() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // ------------------------------------------------------------------ tcgen05
 
 // Shared-memory operand in 128-byte rows with the 128-byte swizzle.  Rows of one 8-row group
@@ -121,13 +133,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t 
 }
 
 // ... leaving alone the tensor-memory lanes whose bit is set in m0 (lanes 0..31) .. m3 (96..127)
-__device__ __forceinline__ void mma_ts_masked(uint32_t d, uint32_t a, Desc b, uint32_t word, uint32_t m0, uint32_t m1, uint32_t m2,
-                                              uint32_t m3, bool add)
+__device__ __forceinline__ void mma_ss_masked(uint32_t d, Desc a, Desc b, uint32_t word, uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3,
+                                              bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, {%6, %7, %8, %9}, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(m0), "r"(m1), "r"(m2), "r"(m3)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, {%7, %8, %9, %10}, p;\n\t}" ::"r"(d),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(m0), "r"(m1), "r"(m2), "r"(m3)
         : "memory");
 }
 

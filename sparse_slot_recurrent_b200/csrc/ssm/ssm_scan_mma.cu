@@ -41,7 +41,7 @@ constexpr int kOutWarps = 8;     // warps that hold the state and write y
 constexpr int kWarps = kInWarps + kOutWarps;
 constexpr int kDtWarps = 2;      // warps that compute step sizes and decays, in alternate chunks
 constexpr int kThreads = (kWarps + 2 + kDtWarps) * 32;
-constexpr int kStgPitch = 80;    // bytes per token row of a warp's y patch: 64 used; conflict-free
+constexpr uint32_t kPatch = 2048;  // a warp's patch of y: 32 tokens x 32 channels, rows of 64 bytes in the 64-byte swizzle
 constexpr size_t kSmemMax = 232448 - 1024;  // the rest: barriers
 
 // per (stage, head) step sizes and decays of a chunk
@@ -67,12 +67,12 @@ __host__ __device__ constexpr Layout layout_of(int N, int HP, bool out)
     l.b_off = 16384;
     l.c_off = l.b_off + nt;
     l.stage_bytes = l.c_off + (out ? nt : 0);
-    const uint32_t fixed = (out ? HP * 16384u + kOutWarps * 32 * kStgPitch : 0);
+    const uint32_t fixed = (out ? HP * 16384u + kOutWarps * kPatch : 0);
     l.stages = 4;
     while (l.stages > 2 && l.stages * (l.stage_bytes + HP * sizeof(Tok)) + fixed + 1024 > kSmemMax) --l.stages;
     l.w_off = l.stages * l.stage_bytes;
     l.stg_off = l.w_off + (out ? HP * 16384u : 0);
-    l.tok_off = l.stg_off + (out ? kOutWarps * 32 * kStgPitch : 0);
+    l.tok_off = l.stg_off + (out ? kOutWarps * kPatch : 0);
     l.total = l.tok_off + l.stages * HP * static_cast<uint32_t>(sizeof(Tok)) + 1024;  // 1024: base alignment
     return l;
 }
@@ -85,7 +85,7 @@ __device__ __forceinline__ float ex2(float v)
 }
 
 struct MmaMaps {
-    CUtensorMap x, b, c;
+    CUtensorMap x, b, c, y;
 };
 
 // N state values, HP heads per 128 channels; OUT: outputs and final state, else what a segment adds to a
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     constexpr Layout L = layout_of(N, HP, OUT);
     constexpr int NB = OUT ? 1 : 2;  // buffers of Xw and dS
     // tensor-memory columns (G shares those of Ya; without outputs dS and Xw have two buffers)
-    constexpr uint32_t cDs = 0, cShi = 128, cSlo = 192, cXw = 256, cX = 352, cYb = 384, cYa = 448;
+    constexpr uint32_t cDs = 0, cShi = 128, cSlo = 192, cXw = 256, cYb = 384, cYa = 448;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bar_mem[kBars];
     __shared__ uint32_t tmem_holder;
@@ -211,16 +211,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             tmem_wait_st();
             done(kXw + i);
             if constexpr (OUT) {
-                if (c > 0) wait(kY, (c - 1) & 1);  // X^T's buffer
-                tmem_fence_after_sync();
-#pragma unroll 1
-                for (int tg = 0; tg < 2; ++tg)
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t xx[4];
-                        ldsm_t(xaddr[half] + st * L.stage_bytes + tg * 2048, xx);
-                        tmem_st_16x8(tq + (static_cast<uint32_t>(half) << 20) + cX + part * 16 + tg * 8, xx[0], xx[1], xx[2], xx[3]);
-                    }
                 wait(kG, c & 1);
                 tmem_fence_after_sync();
                 // tokens j of block q reach tokens i of blocks q..3; this warp takes every second of them
@@ -234,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
 #pragma unroll
                     for (int h = 0; h < HP; ++h) {
                         const Tok& tk = tok[h];
+                        const float skip = (p.D && head0 + h < hg) ? p.D[g * hg + head0 + h] : 0.0f;
                         const uint32_t wbase = L.w_off + h * 16384 + j * 128 + (i0 & 7) * 2;
                         F2 hi[2], lo[2];
 #pragma unroll
@@ -255,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                                 if (cb == q) {
                                     const int ii = i0 + 8 * k - (j + 8 * rb);
                                     un(w, u, v);
-                                    w = f2(ii >= 0 ? u : 0.0f, ii >= -1 ? v : 0.0f);
+                                    // D x_i rides on the diagonal
+                                    w = f2(ii > 0 ? u : ii == 0 ? u + skip : 0.0f, ii > -1 ? v : ii == -1 ? v + skip : 0.0f);
                                 }
                                 const uint32_t at = wbase + rb * 1024 + ((((i0 >> 3) + k) ^ (j & 7)) << 4);
                                 *reinterpret_cast<uint32_t*>(sm + at) = peel(w);
@@ -265,7 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     }
                 }
                 fence_async_smem();
-                tmem_wait_st();
                 done(kW);
             }
             if (++st == L.stages) st = 0, ph ^= 1;
@@ -278,8 +269,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         const int64_t bh = static_cast<int64_t>(b) * p.H + g * hg + ch / p.P;
         const int64_t np = static_cast<int64_t>(N) * p.P;
         const int pc = ch % p.P;
-        const float skip = (OUT && p.D && mine) ? p.D[g * hg + (c0 + q * 32) / p.P] : 0.0f;
-        const F2 skip2 = f2(skip, skip);
         constexpr int NC = N / 2;            // state columns per warp
         constexpr int NV = NC < 16 ? NC : 16;  // of them per tensor-memory access
         F2 S[NC / 2];
@@ -314,73 +303,88 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             tmem_wait_st();
             done(kS);
         }
-        // this lane's 16 bytes of y: token part*32 + lane/4 (+8..), 8 channels
-        const uint32_t patch = L.stg_off + (warp - kInWarps) * 32 * kStgPitch;
-        const int ycol = c0 + q * 32 + (lane & 3) * 8, ytok = part * 32 + (lane >> 2);
-        const int64_t yrow = static_cast<int64_t>(p.H) * p.P;
-        __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.T + r.first + ytok) * yrow + g * cend + ycol;
+        // this warp's patch of y: 32 tokens x 32 channels
+        const uint32_t patch = L.stg_off + (warp - kInWarps) * kPatch;
+        uint32_t paddr[2];  // stmatrix row of this lane, channels half*16..
+#pragma unroll
+        for (int half = 0; half < 2; ++half) paddr[half] = s0 + patch + row * 64 + (((half * 2 + (pcol >> 3)) ^ ((row >> 1) & 3)) << 4);
+        const bool ych = c0 + q * 32 < cend;
         int st = 0;
         uint32_t ph = 0;
         for (int c = 0; c < nch; ++c) {
             const Tok& tok = toks[st * HP + hw];
             wait(kToks + st, ph);
             if constexpr (OUT) {
-                wait(kLanded + st, ph);
+                if (lane == 0) store_read_done();  // the patch is free
+                __syncwarp();
                 wait(kY, c & 1);
                 tmem_fence_after_sync();
-                // y of 32 channels x 32 tokens, through registers into this warp's patch
-#pragma unroll 1
-                for (int tg = 0; tg < 2; ++tg) {
-                    float yb[2][8], ya[2][8];
+                const uint32_t ty = tq + part * 32;
+                float yb[2][8], ya[2][8];
+                tmem_ld_16x16(ty + cYb, yb[0]);
+                tmem_ld_16x16(ty + cYa, ya[0]);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t at = tq + (static_cast<uint32_t>(half) << 20) + part * 32 + tg * 16;
-                        tmem_ld_16x16(at + cYb, yb[half]);
-                        tmem_ld_16x16(at + cYa, ya[half]);
-                    }
+                for (int k4 = 0; k4 < 4; ++k4) {  // 16 tokens k4/2, 16 channels k4%2; the next loads run meanwhile
+                    const int now = k4 & 1, tg = k4 >> 1;
                     const float* e = tok.ein + part * 32 + tg * 16 + 2 * (lane & 3);
                     const float2 e0 = *reinterpret_cast<const float2*>(e), e1 = *reinterpret_cast<const float2*>(e + 8);
-                    const F2 ee[2] = {f2(e0.x, e0.y), f2(e1.x, e1.y)};
                     tmem_wait_ld();
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        settle(yb[half]);
-                        settle(ya[half]);
-                        uint32_t xx[4], o[4];
-                        ldsm_t(xaddr[half] + st * L.stage_bytes + tg * 2048, xx);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {  // 8 tokens k/2, 8 channels k%2
-                            const int at = 4 * (k >> 1) + 2 * (k & 1);
-                            const F2 v = fma2(ee[k >> 1], f2(yb[half][at], yb[half][at + 1]), f2(ya[half][at], ya[half][at + 1]));
-                            o[k] = pack_rn(fma2(skip2, bf_pair(xx[k]), v));
-                        }
-                        stsm_t(s0 + patch + (tg * 16 + row) * kStgPitch + (half * 16 + pcol) * 2, o[0], o[1], o[2], o[3]);
+                    settle(yb[now]);
+                    settle(ya[now]);
+                    if (k4 < 3) {
+                        const uint32_t at = ty + (static_cast<uint32_t>((k4 + 1) & 1) << 20) + ((k4 + 1) >> 1) * 16;
+                        tmem_ld_16x16(at + cYb, yb[now ^ 1]);
+                        tmem_ld_16x16(at + cYa, ya[now ^ 1]);
+                    } else {
+                        done(kYfree);
                     }
-                }
-                done(kYfree);
-                const int nv = min(kQ, r.last - r.first - c * kQ);
+                    uint32_t o[4];
 #pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(sm + patch + ((lane >> 2) + 8 * it) * kStgPitch + (lane & 3) * 16);
-                    if (ytok + 8 * it < nv && ycol < cend) *reinterpret_cast<uint4*>(yp + it * 8 * yrow) = v;
+                    for (int k = 0; k < 4; ++k) {  // 8 tokens k/2, 8 channels k%2
+                        const int at = 4 * (k >> 1) + 2 * (k & 1);
+                        const float2 ee = k < 2 ? e0 : e1;
+                        o[k] = pack_rn(fma2(f2(ee.x, ee.y), f2(yb[now][at], yb[now][at + 1]), f2(ya[now][at], ya[now][at + 1])));
+                    }
+                    stsm_t(paddr[k4 & 1] + tg * 1024, o[0], o[1], o[2], o[3]);
                 }
-                yp += kQ * yrow;
+                const int tok0 = r.first + c * kQ + part * 32, left = r.last - tok0;
+                if (left >= 32) {
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && ych) tma_store_3d(&maps.y, g * cend + c0 + q * 32, tok0, b, s0 + patch);
+                } else {  // rows behind the sequence are not this call's to write
+                    __syncwarp();
+                    const int64_t yrow = static_cast<int64_t>(p.H) * p.P;
+                    __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.T + tok0) * yrow + g * cend + c0 +
+                                        q * 32 + (lane & 3) * 8;
+#pragma unroll 1
+                    for (int t = lane >> 2; t < left && ych; t += 8)
+                        *reinterpret_cast<uint4*>(yp + t * yrow) =
+                            *reinterpret_cast<const uint4*>(sm + patch + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+                    __syncwarp();
+                }
             }
             // S' = dec S + dS
             const int i = NB == 2 ? c & 1 : 0;
             wait(kDs + i, NB == 2 ? (c >> 1) & 1 : c & 1);
             tmem_fence_after_sync();
             const F2 dec = f2(tok.dec, tok.dec);
+            const uint32_t td = tq + cDs + i * 128 + part * NC;
+            float d[2][NV];
+            tmem_ld_cols<NV>(td, d[0]);
 #pragma unroll
             for (int k0 = 0; k0 < NC; k0 += NV) {
-                float d[NV];
-                tmem_ld_cols<NV>(tq + cDs + i * 128 + part * NC + k0, d);
+                const int now = (k0 / NV) & 1;
                 tmem_wait_ld();
-                settle(d);
+                settle(d[now]);
+                if (k0 + NV < NC) tmem_ld_cols<NV>(td + k0 + NV, d[now ^ 1]);
+                else done(kDsFree + i);  // the next chunk's dS may come while the state is split below
 #pragma unroll
-                for (int k = 0; k < NV / 2; ++k) S[k0 / 2 + k] = fma2(S[k0 / 2 + k], dec, f2(d[2 * k], d[2 * k + 1]));
-                if (k0 + NV == NC) done(kDsFree + i);
-                if (OUT && c + 1 < nch) put_state(k0);
+                for (int k = 0; k < NV / 2; ++k) S[k0 / 2 + k] = fma2(S[k0 / 2 + k], dec, f2(d[now][2 * k], d[now][2 * k + 1]));
+            }
+            if (OUT && c + 1 < nch) {
+#pragma unroll
+                for (int k0 = 0; k0 < NC; k0 += NV) put_state(k0);
             }
             if (OUT && c + 1 < nch) {
                 tmem_wait_st();
@@ -390,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             if (lane == 0) arrive(bar(kEmpty + st));
             if (++st == L.stages) st = 0, ph ^= 1;
         }
+        if (OUT && lane == 0) store_done();
         float* to = nullptr;
         if (mine) {
             if (!OUT) to = p.seg_state + (bh * p.split.slots() + seg) * np;
@@ -445,12 +450,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         // ------------------------------------------------------------ MMA issue (whole warp, one lane issues)
         regs_down<kMiscRegs>();
         constexpr uint32_t wG = mma_word(64, 64, false, false), wYb = mma_word(128, 64, false, false);
-        constexpr uint32_t wYa = mma_word(128, 64, false, true), wDs = mma_word(128, N, false, true);
+        constexpr uint32_t wYa = mma_word(128, 64, true, true), wDs = mma_word(128, N, false, true);
         const Desc wdesc = desc_of(s0 + L.w_off, 8192);
+        auto add_chunk = [&](int c, int st) {  // dS of chunk c
+            const Desc down = desc_of(s0 + st * L.stage_bytes + L.b_off, 8192);  // B as [j, n]: contraction down the rows
+            const int i = NB == 2 ? c & 1 : 0;
+            wait(kXw + i, NB == 2 ? (c >> 1) & 1 : c & 1);
+            if (c >= NB) wait(kDsFree + i, NB == 2 ? ((c >> 1) - 1) & 1 : (c - 1) & 1);
+            tmem_fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int s = 2; s >= 0; --s)  // the small pieces first
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_ts(tm + cDs + i * 128, tm + cXw + i * 96 + s * 32 + k * 8, down + k * 2048, wDs, s < 2 || k > 0);
+                mma_commit(bar(kDs + i));
+            }
+            __syncwarp();
+        };
         int st = 0;
         uint32_t ph = 0;
         for (int c = 0; c < nch; ++c) {
-            const Desc down = desc_of(s0 + st * L.stage_bytes, 8192);  // contraction down the rows: x, B as [j, n]
+            const Desc down = desc_of(s0 + st * L.stage_bytes, 8192);  // x as [j, p]: contraction down the rows
             const Desc along = desc_of(s0 + st * L.stage_bytes, 16);   // contraction along the rows: B and C as [., n]
             wait(kLanded + st, ph);
             if (r.last - r.first - c * kQ < kQ) wait(kFixed, 0);
@@ -468,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                 __syncwarp();
             }
             if constexpr (OUT) {
+                add_chunk(c, st);
                 wait(kS, c & 1);
                 tmem_fence_after_sync();
                 if (elect_one()) {
@@ -487,31 +509,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                         for (int s = 0; s < 2; ++s)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const Desc db = wdesc + (h * 16384 + (s ? 0 : 8192) + k * 2048);
+                                const Desc da = down + k * 2048, db = wdesc + (h * 16384 + (s ? 0 : 8192) + k * 2048);
                                 if constexpr (HP == 1) {
-                                    mma_ts(tm + cYa, tm + cX + k * 8, db, wYa, s + k > 0);
+                                    mma_ss(tm + cYa, da, db, wYa, s + k > 0);
                                 } else {
                                     auto off = [&](int qq) { return (HP == 4 ? qq : qq >> 1) == h ? 0u : 0xffffffffu; };
-                                    mma_ts_masked(tm + cYa, tm + cX + k * 8, db, wYa, off(0), off(1), off(2), off(3), s + k > 0);
+                                    mma_ss_masked(tm + cYa, da, db, wYa, off(0), off(1), off(2), off(3), s + k > 0);
                                 }
                             }
                     mma_commit(bar(kY));
                 }
                 __syncwarp();
             }
-            const int i = NB == 2 ? c & 1 : 0;
-            wait(kXw + i, NB == 2 ? (c >> 1) & 1 : c & 1);
-            if (c >= NB) wait(kDsFree + i, NB == 2 ? ((c >> 1) - 1) & 1 : (c - 1) & 1);
-            tmem_fence_after_sync();
-            if (elect_one()) {
-#pragma unroll
-                for (int s = 2; s >= 0; --s)  // the small pieces first
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_ts(tm + cDs + i * 128, tm + cXw + i * 96 + s * 32 + k * 8, down + (L.b_off + k * 2048), wDs, s < 2 || k > 0);
-                mma_commit(bar(kDs + i));
-            }
-            __syncwarp();
+            if constexpr (!OUT) add_chunk(c, st);
             if (++st == L.stages) st = 0, ph ^= 1;
         }
         if (*abort_flag && lane == 0) {  // tensor memory is given back only when nothing writes to it
@@ -617,19 +627,19 @@ EncodeFn encoder()
     return fn;
 }
 
-// 64 tokens x 64 elements of a bf16 operand: dims inner (contiguous), then (size, stride in elements).
-bool encode(CUtensorMap* map, const void* base, int rank, const int64_t* size, const int64_t* stride)
+// Boxes of `rows` tokens x `inner` elements (64 with the 128-byte swizzle, 32 with the 64-byte one) of a bf16 operand: dims inner (contiguous), then (size, stride in elements).
+bool encode(CUtensorMap* map, const void* base, int rank, const int64_t* size, const int64_t* stride, int inner = 64, int rows = 64)
 {
     cuuint64_t dims[4], bytes[3];
     cuuint32_t box[4], one[4] = {1, 1, 1, 1};
     for (int i = 0; i < rank; ++i) {
         dims[i] = static_cast<cuuint64_t>(size[i]);
-        box[i] = i == 0 || i == rank - 2 ? 64 : 1;
+        box[i] = i == 0 ? inner : i == rank - 2 ? rows : 1;
         // the stride of a single element is never used
         if (i > 0) bytes[i - 1] = size[i] == 1 ? 16 : static_cast<cuuint64_t>(stride[i]) * 2;
     }
     return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, bytes, box, one,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, inner == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -637,7 +647,8 @@ bool map_operands(const SsmParams& p, MmaMaps* m)
 {
     const int64_t xsize[3] = {static_cast<int64_t>(p.H) * p.P, p.T, p.B}, xstr[3] = {1, p.xs.t, p.xs.b};
     const int64_t bsize[4] = {p.N, p.G, p.T, p.B}, bstr[4] = {1, p.bs.h, p.bs.t, p.bs.b}, cstr[4] = {1, p.cs.h, p.cs.t, p.cs.b};
-    return encode(&m->x, p.x, 3, xsize, xstr) && encode(&m->b, p.Bm, 4, bsize, bstr) && encode(&m->c, p.Cm, 4, bsize, cstr);
+    const int64_t ystr[3] = {1, xsize[0], xsize[0] * p.T};
+    return encode(&m->y, p.y, 3, xsize, ystr, 32, 32) && encode(&m->x, p.x, 3, xsize, xstr) && encode(&m->b, p.Bm, 4, bsize, bstr) && encode(&m->c, p.Cm, 4, bsize, cstr);
 }
 
 template <int N, int HP, bool OUT>
