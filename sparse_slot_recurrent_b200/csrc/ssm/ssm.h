@@ -53,6 +53,21 @@ struct SsmSplit {
     __host__ __device__ int slots() const { return pieces() + 1; }  // states per (sequence, head) in the workspace
 };
 
+// Step sizes and decays of 64 tokens of one head, for the tensor-core form.  With a_i the sum of d A over the
+// chunk's tokens up to i, in powers of two (times log2 e); blocks are 16 tokens.
+struct ChunkTok {
+    float hi[64], lo[64];  // a_i as the sum of two floats
+    float d[64];           // step sizes
+    float ein[64];         // 2^a_i
+    float w[64];           // 2^(a_63 - a_j) d_j
+    float u[64];           // 2^(a_i - sum before i's block)
+    float v[64];           // 2^(sum up to the end of j's block - a_j) d_j
+    float dec;             // 2^a_63
+    float blk[3];          // 2^ the sums of blocks 1 and 2, and of both
+    double total, pad;     // a_63
+};
+constexpr int kChunk = 64;
+
 struct SsmParams {
     const void* x;  // [B,T,H,P]
     Str3 xs;
@@ -77,8 +92,9 @@ struct SsmParams {
     SsmSplit split;
     float* seg_state;  // [B,H,slots,N,P]: what piece i adds; then, in slot k*sub, the state segment k starts from
     float* seg_decay;  // [B,H,pieces]
+    ChunkTok* toks;    // [B,H,ceil(T/64)], the tensor-core form only
     uint32_t* status;
-    uint64_t wait_ns;
+    int64_t chain_first;  // first (sequence, head) of a launch of the chaining kernel
 };
 
 struct SsmStepParams {

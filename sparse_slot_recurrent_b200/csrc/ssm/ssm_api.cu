@@ -74,13 +74,20 @@ bool take_strides(const ramnet_strides* s, int64_t B, int64_t T, int64_t H, int6
 
 size_t state_bytes(const ramnet_ssm_config* c, int64_t B) { return sizeof(float) * B * c->H * c->N * c->P; }
 
-size_t ssm_workspace(const ramnet_ssm_config* c, int32_t B, int32_t T, ramnet::SsmSplit* split, size_t* decay_off)
+// The workspace: step sizes and decays by chunk of 64 tokens, then, where sequences are cut, the pieces' states
+// and their decays.
+struct Workspace {
+    size_t state_off, decay_off, total;
+};
+
+Workspace ssm_workspace(const ramnet_ssm_config* c, int64_t B, int64_t T, const ramnet::SsmSplit& split)
 {
-    *split = ramnet::ssm_split(B, T, c->H, c->G, c->P);
-    *decay_off = 0;
-    if (split->nseg <= 1) return 0;
-    *decay_off = state_bytes(c, B) * split->slots();
-    return *decay_off + sizeof(float) * static_cast<size_t>(B) * c->H * split->pieces();
+    Workspace w;
+    const size_t heads = static_cast<size_t>(B) * c->H;
+    w.state_off = heads * ((T + ramnet::kChunk - 1) / ramnet::kChunk) * sizeof(ramnet::ChunkTok);
+    w.decay_off = w.state_off + (split.nseg > 1 ? state_bytes(c, B) * split.slots() : 0);
+    w.total = w.decay_off + (split.nseg > 1 ? sizeof(float) * heads * split.pieces() : 0);
+    return w;
 }
 
 }  // namespace
@@ -91,9 +98,7 @@ size_t ramnet_ssm_workspace_bytes(const ramnet_ssm_config* cfg, int32_t B, int32
 {
     ramnet::set_last_error(RAMNET_OK, "");
     if (check_ssm(cfg, B, T) != RAMNET_OK) return 0;
-    ramnet::SsmSplit split;
-    size_t off;
-    return ssm_workspace(cfg, B, T, &split, &off);
+    return ssm_workspace(cfg, B, T, ramnet::ssm_split(B, T, cfg->H, cfg->G, cfg->P)).total;
 }
 
 ramnet_status ramnet_ssm_forward(const ramnet_ssm_config* cfg, int32_t B, int32_t T, ramnet_dtype in_dt, const void* x,
@@ -124,20 +129,19 @@ ramnet_status ramnet_ssm_forward(const ramnet_ssm_config* cfg, int32_t B, int32_
     MAY(S_in, 16);
     NEED(y, 16);
     NEED(S_out, 16);
-    size_t off;
-    const size_t need = ssm_workspace(cfg, B, T, &p.split, &off);
-    if (need > 0) {
-        NEED(workspace, 16);
-        CHECK(workspace_bytes >= need, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
-        p.seg_state = static_cast<float*>(workspace);
-        p.seg_decay = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + off);
-    }
+    p.split = ramnet::ssm_split(B, T, cfg->H, cfg->G, cfg->P);
+    const Workspace ws = ssm_workspace(cfg, B, T, p.split);
+    NEED(workspace, 16);
+    CHECK(workspace_bytes >= ws.total, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.total);
+    unsigned char* base = static_cast<unsigned char*>(workspace);
+    p.toks = reinterpret_cast<ramnet::ChunkTok*>(base);
+    p.seg_state = reinterpret_cast<float*>(base + ws.state_off);
+    p.seg_decay = reinterpret_cast<float*>(base + ws.decay_off);
     p.x = x, p.dt = dt, p.A = A, p.Bm = Bm, p.Cm = Cm, p.D = D, p.dt_bias = dt_bias;
     p.in_bf16 = in_dt == RAMNET_BF16, p.out_bf16 = out_dt == RAMNET_BF16;
     p.lengths = lengths, p.S_in = S_in, p.y = y, p.S_out = S_out;
     p.B = B, p.T = T, p.H = cfg->H, p.G = cfg->G, p.N = cfg->N, p.P = cfg->P;
     p.softplus = cfg->dt_softplus != 0, p.dt_min = cfg->dt_min, p.dt_max = cfg->dt_max;
-    p.wait_ns = 2000000000ull;
     p.status = ramnet::library_status_word();
     if (p.status == nullptr) return launched(cudaGetLastError(), "status word");
     return launched(ramnet::launch_ssm_scan(p, static_cast<cudaStream_t>(stream)), "ssm_forward launch");

@@ -27,6 +27,19 @@ __device__ __forceinline__ SegRange seg_range(int len, int seg, int seg_len)
     return r;
 }
 
+// 2^x, rounded once: a bias of the hardware's exp2, a fraction of an ulp, would add up over the hundreds of
+// chunks that a slowly decaying state remembers.  Taylor series of 2^f, |f| <= 1/2, in 64 bits (error below 1e-11).
+__device__ __forceinline__ float exp2_of(double x)
+{
+    x = fmin(fmax(x, -160.0), 160.0);
+    const double n = rint(x), f = (x - n) * 0.69314718055994530942;
+    double r = 1.0 / 362880;
+    const double inv[9] = {1.0 / 40320, 1.0 / 5040, 1.0 / 720, 1.0 / 120, 1.0 / 24, 1.0 / 6, 0.5, 1.0, 1.0};
+#pragma unroll
+    for (int i = 0; i < 9; ++i) r = fma(r, f, inv[i]);
+    return ldexpf(static_cast<float>(r), static_cast<int>(n));
+}
+
 __device__ __forceinline__ int seq_len(const int32_t* lengths, int b, int T)
 {
     return lengths ? min(max(lengths[b], 0), T) : T;

@@ -31,16 +31,29 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-// Bounded wait for phase `parity`: at most limit_ns, after which the block's abort flag is raised and
-// every wait returns at once (the kernel reports the flag in the status word at its end).  Short,
-// because it is inlined at every hand-over and the roles of a block compete for the instruction cache.
-__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns)
+// Bounded wait for phase `parity`: at most kPolls polls, each of which the hardware suspends for up to some
+// microseconds (measured: 4), about two seconds in all.  When they run out the block's abort flag (a word of
+// shared memory) is raised, after which every wait of the block returns at once; the kernel reports the flag in
+// the status word at its end.  Few instructions, because this is inlined at every hand-over and the roles of a
+// block share the instruction cache.
+constexpr uint32_t kPolls = 1u << 19;
+__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, uint32_t abort_addr)
 {
-    if (try_wait(bar, parity)) return;
-    const uint64_t t0 = now_ns();
-#pragma unroll 1
-    while (!try_wait(bar, parity) && !*abort_flag)
-        if (now_ns() - t0 > limit_ns) *abort_flag = 1;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .u32 n, a;\n\tmov.u32 n, %3;\n"
+        "L_poll_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%0], %1;\n\t"
+        "@p bra L_done_%=;\n\t"
+        "ld.volatile.shared.u32 a, [%2];\n\t"
+        "setp.ne.u32 p, a, 0;\n\t"
+        "@p bra L_done_%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 p, n, 0;\n\t"
+        "@p bra L_poll_%=;\n\t"
+        "st.volatile.shared.u32 [%2], 1;\n"
+        "L_done_%=:\n\t}" ::"r"(bar),
+        "r"(parity), "r"(abort_addr), "n"(kPolls)
+        : "memory");
 }
 
 __device__ __forceinline__ void arrive(uint32_t bar)
@@ -82,6 +95,13 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int c0, int
 }
 __device__ __forceinline__ void store_read_done() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// ... and plain bytes (both addresses and the size in units of 16)
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 
 // ------------------------------------------------------------------ tcgen05
 
@@ -140,6 +160,20 @@ __device__ __forceinline__ void mma_ss_masked(uint32_t d, Desc a, Desc b, uint32
         "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, {%7, %8, %9, %10}, p;\n\t}" ::"r"(d),
         "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(m0), "r"(m1), "r"(m2), "r"(m3)
+        : "memory");
+}
+
+// ... with both operands fp32 taken as tf32 (10 bits behind the leading one, the rest cut off)
+__host__ __device__ constexpr uint32_t mma_word_tf32(int M, int N)
+{
+    return (1u << 4) | (2u << 7) | (2u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ts_tf32(uint32_t d, uint32_t a, Desc b, uint32_t word, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add))
         : "memory");
 }
 

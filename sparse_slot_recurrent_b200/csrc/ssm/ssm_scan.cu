@@ -111,17 +111,31 @@ __global__ void __launch_bounds__(128) k_ssm_scan(SsmParams p)
 }
 
 // Turns what the pieces add into the states the segments start from, in token order; four
-// neighbouring state values per thread, one (sequence, head) per blockIdx.y.
+// neighbouring state values per thread, one (sequence, head) per blockIdx.y.  With chunk totals the
+// pieces' decays come from those, else from seg_decay.
 __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
 {
+    __shared__ float decay[256];
     const int np4 = p.N * p.P / 4;
     const int e = blockIdx.x * 256 + threadIdx.x;
-    if (e >= np4) return;
     const int64_t bh = blockIdx.y;
+    const int n = p.split.pieces(), sub = p.split.sub;
+    for (int k = threadIdx.x; k < n; k += 256) {
+        if (p.toks) {
+            const int chunks = (p.T + kChunk - 1) / kChunk, per = p.split.piece_len() / kChunk;
+            const int b = static_cast<int>((bh + p.chain_first) / p.H);
+            const int have = (seq_len(p.lengths, b, p.T) + kChunk - 1) / kChunk;  // chunks that the sequence has
+            double sum = 0.0;
+            for (int i = k * per; i < min((k + 1) * per, have); ++i) sum += p.toks[bh * chunks + i].total;
+            decay[k] = exp2_of(sum);
+        } else {
+            decay[k] = p.seg_decay[bh * n + k];
+        }
+    }
+    __syncthreads();
+    if (e >= np4) return;
     float4 s = p.S_in ? reinterpret_cast<const float4*>(p.S_in)[bh * np4 + e] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float4* at = reinterpret_cast<float4*>(p.seg_state) + bh * p.split.slots() * np4 + e;
-    const float* decay = p.seg_decay + bh * p.split.pieces();
-    const int n = p.split.pieces(), sub = p.split.sub;
 #pragma unroll 4
     for (int k = 0; k < n; ++k, at += np4) {
         const float4 add = *at;
@@ -160,6 +174,8 @@ cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t s)
         if (p.S_in) q.S_in = p.S_in + at * np;
         q.seg_state = p.seg_state + at * p.split.slots() * np;
         q.seg_decay = p.seg_decay + at * p.split.pieces();
+        if (p.toks) q.toks = p.toks + at * ((p.T + kChunk - 1) / kChunk);
+        q.chain_first = at;
         const int64_t rows = bh - at < 65535 ? bh - at : 65535;
         k_ssm_chain<<<dim3(static_cast<unsigned>((np / 4 + 255) / 256), static_cast<unsigned>(rows)), 256, 0, s>>>(q);
     }
@@ -183,9 +199,8 @@ SsmSplit ssm_split(int B, int T, int H, int G, int P)
     return s;
 }
 
-cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t s)
+cudaError_t launch_ssm_plain(const SsmParams& p, cudaStream_t s)
 {
-    if (ssm_mma_takes(p)) return launch_ssm_mma(p, s);
     switch (p.N) {
         case 16: return go<16>(p, s);
         case 32: return go<32>(p, s);
@@ -194,6 +209,14 @@ cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t s)
         case 256: return go<256>(p, s);
         default: return cudaErrorInvalidValue;
     }
+}
+
+cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t s)
+{
+    if (ssm_mma_takes(p)) return launch_ssm_mma(p, s);
+    SsmParams q = p;
+    q.toks = nullptr;
+    return launch_ssm_plain(q, s);
 }
 
 }  // namespace ramnet

@@ -6,28 +6,29 @@
 //   S'   = exp(a_63) S + sum_j (exp(a_63 - a_j) d_j x_j) (x) B_j
 // so a chunk is four products.  All are taken transposed, with 128 channels p of one group's heads
 // (128/P heads) down the 128 lanes of tensor memory:
-//   G^T [j,i] = B C^T             both from shared memory, M = 64
-//   Yb  [p,i] = S^T C^T           S^T in tensor memory as two bf16 pieces
-//   Ya  [p,i] = X^T W^T           W[i,j] = exp(a_i - a_j) d_j G[i,j], two bf16 pieces in shared memory,
-//                                 one product per head with the other heads' lanes switched off
-//   dS  [p,n] = Xw^T B            Xw = exp(a_63 - a_j) d_j x_j in tensor memory, three bf16 pieces
-// and y^T = exp(a_i) Yb + Ya + D x^T.  The tiles of x, B and C are used as they arrive by TMA, B and C in
-// both roles; x is transposed on the way to registers (ldmatrix.trans) and y on the way back.
+//   G^T [j,i] = B C^T      bf16, both from shared memory, M = 64
+//   Ya  [p,i] = X^T W^T    W[i,j] = exp(a_i - a_j) d_j G[i,j] (+ D on the diagonal) as two bf16 pieces in shared
+//                          memory, one product per head with the other heads' lanes switched off
+//   Yb  [p,i] = S^T C^T    tf32: S^T in tensor memory as it is, C widened to 32 bits in shared memory
+//   dS  [p,n] = Xw^T B     Xw = exp(a_63 - a_j) d_j x_j in tensor memory as three bf16 pieces
+// and y^T = exp(a_i) Yb + Ya.  The tiles of x, B and C are used as they arrive by TMA, B and C in both
+// roles; x is transposed on the way to registers (ldmatrix.trans) and y on the way back.
 //
 // Precision.  The state itself stays in fp32 registers and takes dS with one fused multiply-add
 // per chunk (the tensor core's accumulation would shave a bit off a long-lived state every
-// chunk).  Xw is exact in three pieces of 8 bits; S and W as operands of a bf16 result carry 16
-// bits, 2^-16 of each value against the result's 2^-9.  Sums of d A are taken in 64 bits; a_i - a_j is the
-// difference of two float pairs, so strong decay early in a chunk costs later tokens nothing.
+// chunk).  Xw is exact in three pieces of 8 bits.  As operands of a bf16 result W carries 16 bits and S 11: 2^-16 and
+// 2^-10 of each value, against the result's own 2^-9.  Sums of d A are taken in 64 bits; a_i - a_j is the
+// difference of two float pairs within a block of 16 tokens, and between blocks a product of factors that meet at
+// block ends, so strong decay early in a chunk costs later tokens nothing.
 //
-// Work split.  One CTA per (sequence, 128 channels, segment of the sequence), chunks in order; 16
-// warps do the elementwise work of a chunk, each on 32 channels x 16 tokens (or N/4 state columns), one
-// warp feeds TMA, one issues MMAs, one computes step sizes and decays.  Per chunk the order
-//   W -> [MMA Ya] Xw -> [MMA dS] y -> [MMA G of the next chunk] S -> [MMA Yb] ...
-// puts elementwise work of the same warps behind every MMA's latency.
-// Bound: issue slots of the elementwise work (about 500 instructions per warp and chunk).
-#include <mutex>
-
+// Work split.  A first small launch turns dt into step sizes and decays by chunk (k_ssm_decay).  Then one CTA per
+// (sequence, 128 channels, segment of the sequence), chunks in order, warps by role:
+//   0-7   operands: Xw and W, C in 32 bits;   8-15  state (32 channels x N/2 values each) and outputs;
+//   16    TMA loads and stores;  18 issues G and dS, 19 Yb and Ya.
+// The state's chain Y -> outputs read -> state stored -> Yb -> Y is what a chunk cannot go below; the rest overlaps.
+// The code of all roles has to stay within the instruction cache (about 32 KB of loops here): unrolling them fully
+// made every role wait for instructions and cost a third of the speed.
+// Bound: issue slots of the elementwise work, and the tensor pipe (about 1900 cycles per chunk at N = 128).
 #include "ssm_mma.cuh"
 
 namespace ramnet {
@@ -35,29 +36,21 @@ namespace {
 
 // Registers per thread by role: 20 warps launch with 96 each, and 2 x 80 + 2 x 128 + 64 = 5 x 96.
 constexpr int kInRegs = 80, kOutRegs = 128, kMiscRegs = 64;
-constexpr int kQ = 64;           // tokens per chunk
-constexpr int kInWarps = 8;      // warps that prepare operands (W, Xw)
-constexpr int kOutWarps = 8;     // warps that hold the state and write y
-constexpr int kWarps = kInWarps + kOutWarps;
-constexpr int kDtWarps = 2;      // warps that compute step sizes and decays, in alternate chunks
-constexpr int kThreads = (kWarps + 2 + kDtWarps) * 32;
-constexpr uint32_t kPatch = 2048;  // a warp's patch of y: 32 tokens x 32 channels, rows of 64 bytes in the 64-byte swizzle
+constexpr int kQ = kChunk;       // tokens per chunk
+constexpr int kInWarps = 8, kOutWarps = 8, kWarps = kInWarps + kOutWarps;
+constexpr int kLoadWarp = 16, kMmaWarp = 18;
+constexpr int kThreads = 20 * 32;
+constexpr uint32_t kPatch = 4096;  // y of 64 tokens x 32 channels, rows of 64 bytes in the 64-byte swizzle
 constexpr size_t kSmemMax = 232448 - 1024;  // the rest: barriers
 
-// per (stage, head) step sizes and decays of a chunk
-struct Tok {
-    float4 t[kQ];    // a_j log2(e) as a float pair, d_j, exp(a_63 - a_j) d_j
-    float hi[kQ], lo[kQ];  // the same pair, by token
-    float ein[kQ];   // exp(a_i)
-    float w[kQ];     // exp(a_63 - a_j) d_j
-    float dec, pad[3];     // exp(a_63)
-};
-
-enum Bar { kLanded = 0, kToks = 4, kEmpty = 8, kFixed = 12, kG, kW, kY, kYfree, kS, kXw, kDs = kXw + 2, kDsFree = kDs + 2, kDrain = kDsFree + 2, kBars };
+// Hand-overs.  Without outputs two chunks are in flight and alternate between two barriers of a kind; elsewhere
+// each side of a hand-over waits for the other before the next, so no waiting warp is ever a phase behind.
+enum Bar { kLanded = 0, kEmpty = 4, kFixed = 8, kG, kW, kC, kY, kS, kOut, kPatchFree, kXw, kDs = kXw + 2, kDsFree = kDs + 2,
+           kDrain = kDsFree + 2, kBars = kDrain + 2 };
 
 struct Layout {
     int stages;
-    uint32_t b_off, c_off, stage_bytes, w_off, stg_off, tok_off, total;
+    uint32_t b_off, c_off, stage_bytes, w_off, c32_off, patch_off, tok_off, total;
 };
 
 __host__ __device__ constexpr Layout layout_of(int N, int HP, bool out)
@@ -67,13 +60,15 @@ __host__ __device__ constexpr Layout layout_of(int N, int HP, bool out)
     l.b_off = 16384;
     l.c_off = l.b_off + nt;
     l.stage_bytes = l.c_off + (out ? nt : 0);
-    const uint32_t fixed = (out ? HP * 16384u + kOutWarps * kPatch : 0);
+    const uint32_t w = out ? HP * 16384u : 0, c32 = out ? (N + 31) / 32 * 8192u : 0, patch = out ? 4 * kPatch : 0;
+    const uint32_t tok = HP * static_cast<uint32_t>(sizeof(ChunkTok));
     l.stages = 4;
-    while (l.stages > 2 && l.stages * (l.stage_bytes + HP * sizeof(Tok)) + fixed + 1024 > kSmemMax) --l.stages;
+    while (l.stages > 2 && l.stages * (l.stage_bytes + tok) + w + c32 + patch + 1024 > kSmemMax) --l.stages;
     l.w_off = l.stages * l.stage_bytes;
-    l.stg_off = l.w_off + (out ? HP * 16384u : 0);
-    l.tok_off = l.stg_off + (out ? kOutWarps * kPatch : 0);
-    l.total = l.tok_off + l.stages * HP * static_cast<uint32_t>(sizeof(Tok)) + 1024;  // 1024: base alignment
+    l.c32_off = l.w_off + w;
+    l.patch_off = l.c32_off + c32;
+    l.tok_off = l.patch_off + patch;
+    l.total = l.tok_off + l.stages * tok + 1024;  // 1024: base alignment
     return l;
 }
 
@@ -84,66 +79,118 @@ __device__ __forceinline__ float ex2(float v)
     return r;
 }
 
+// Step sizes and decays of every chunk: one warp per (sequence, head, chunk), two tokens per lane, sums in 64 bits.
+__global__ void __launch_bounds__(256) k_ssm_decay(const SsmParams p, int chunks, int64_t work)
+{
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (id >= work) return;
+    const int lane = threadIdx.x & 31;
+    // neighbouring warps take neighbouring heads, whose dt share sectors
+    const int h = static_cast<int>(id % p.H);
+    const int64_t bc = id / p.H;
+    const int c = static_cast<int>(bc % chunks), b = static_cast<int>(bc / chunks);
+    const int len = seq_len(p.lengths, b, p.T), t0 = c * kQ;
+    if (t0 >= len) return;
+    const float bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
+    const double A = static_cast<double>(p.A[h]) * 1.4426950408889634074;
+    float d[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int t = t0 + 2 * lane + k;
+        d[k] = 0.0f;  // a token that is not there neither decays nor writes
+        if (t < len) d[k] = step_size(load_in(p.dt, static_cast<size_t>(b * p.dts.b + t * p.dts.t + h * p.dts.h), 1), bias, p.softplus, p.dt_min, p.dt_max);
+    }
+    const double a1 = d[1] * A;
+    double sum = d[0] * A + a1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+    }
+    const double total = __shfl_sync(0xffffffffu, sum, 31);
+    const double blk_end = __shfl_sync(0xffffffffu, sum, lane | 7);
+    double blk_start = __shfl_sync(0xffffffffu, sum, ((lane & 24) - 1) & 31);
+    if (lane < 8) blk_start = 0.0;
+    const double end1 = __shfl_sync(0xffffffffu, sum, 23), end0 = __shfl_sync(0xffffffffu, sum, 7);
+    ChunkTok& tk = p.toks[(static_cast<int64_t>(b) * p.H + h) * chunks + c];
+    float hi[2], lo[2], e[2], w[2], u[2], v[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const double cum = k ? sum : sum - a1;
+        hi[k] = static_cast<float>(cum);
+        lo[k] = static_cast<float>(cum - static_cast<double>(hi[k]));
+        e[k] = exp2f(hi[k]);
+        w[k] = d[k] * exp2f(static_cast<float>(total - cum));
+        u[k] = exp2f(static_cast<float>(cum - blk_start));
+        v[k] = d[k] * exp2f(static_cast<float>(blk_end - cum));
+    }
+    auto put = [&](float* at, const float (&x)[2]) { reinterpret_cast<float2*>(at)[lane] = make_float2(x[0], x[1]); };
+    put(tk.hi, hi);
+    put(tk.lo, lo);
+    put(tk.d, d);
+    put(tk.ein, e);
+    put(tk.w, w);
+    put(tk.u, u);
+    put(tk.v, v);
+    if (lane == 0) {
+        tk.dec = exp2_of(total);
+        tk.blk[2] = exp2f(static_cast<float>(end1 - end0));
+        tk.total = total;
+    }
+    if (lane == 8 || lane == 16) tk.blk[(lane >> 3) - 1] = exp2f(static_cast<float>(blk_end - blk_start));
+}
+
 struct MmaMaps {
     CUtensorMap x, b, c, y;
 };
 
-// N state values, HP heads per 128 channels; OUT: outputs and final state, else what a segment adds to a
-// zero state.
-template <int N, int HP, bool OUT>
+// N state values, heads of P channels, HP of them per 128 channels; OUT: outputs and final state, else what a piece
+// of the sequence adds to a zero state.
+template <int N, int P, bool OUT>
 __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__ MmaMaps maps, const SsmParams p, int tiles)
 {
+    constexpr int HP = P >= 128 ? 1 : 128 / P;
     constexpr Layout L = layout_of(N, HP, OUT);
-    constexpr int NB = OUT ? 1 : 2;  // buffers of Xw and dS
-    // tensor-memory columns (G shares those of Ya; without outputs dS and Xw have two buffers)
-    constexpr uint32_t cDs = 0, cShi = 128, cSlo = 192, cXw = 256, cYb = 384, cYa = 448;
+    constexpr int HALVES = OUT && N == 128 ? 2 : 1;  // dS comes in halves of 64 columns where tensor memory is short
+    // tensor-memory columns
+    constexpr uint32_t cDs = 0, cS = 64, cXw = OUT ? 192 : 256, cYb = 288, cYa = 352, cG = 416;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bar_mem[kBars];
     __shared__ uint32_t tmem_holder;
     __shared__ int abort_mem;
-    __shared__ double log_mem[kDtWarps][HP];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t s0 = smem_addr(sm), bars = smem_addr(bar_mem);
-    Tok* toks = reinterpret_cast<Tok*>(sm + L.tok_off);
+    ChunkTok* toks = reinterpret_cast<ChunkTok*>(sm + L.tok_off);
     volatile int* abort_flag = &abort_mem;
+    const uint32_t abort_addr = smem_addr(&abort_mem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // which channels and tokens
     const int tile = static_cast<int>(blockIdx.x % tiles);
     const int bg = static_cast<int>(blockIdx.x / tiles);
     const int g = bg % p.G, b = bg / p.G, seg = blockIdx.y;
-    const int hg = p.H / p.G, c0 = tile * 128, cend = hg * p.P;  // channels [c0, min(c0+128, cend)) of the group
+    const int hg = p.H / p.G, c0 = tile * 128, cend = hg * P;  // channels [c0, min(c0+128, cend)) of the group
     const SegRange r = seg_range(seq_len(p.lengths, b, p.T), seg, OUT ? p.split.seg_len : p.split.piece_len());
     const int nch = (r.last - r.first + kQ - 1) / kQ;
-    const int head0 = c0 / p.P;  // first head, within the group
+    const bool ragged = (r.last - r.first) % kQ != 0;  // the last chunk is not full
+    const int head0 = c0 / P;                          // first head, within the group
 
     auto bar = [&](int i) { return bars + 8u * i; };
-    auto wait = [&](int i, uint32_t parity) {
-        wait_phase(bars + 8u * i, parity, abort_flag, p.wait_ns);
-    };
+    auto wait = [&](int i, uint32_t parity) { wait_phase(bars + 8u * i, parity, abort_addr); };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(bar_mem + kLanded + i, 1);
-            mbar_init(bar_mem + kToks + i, 1);
-            mbar_init(bar_mem + kEmpty + i, kOutWarps);
-        }
-        mbar_init(bar_mem + kFixed, 1);
-        mbar_init(bar_mem + kG, 1);
-        mbar_init(bar_mem + kDrain, 1);
-        mbar_init(bar_mem + kW, kInWarps);
-        mbar_init(bar_mem + kY, 1);
-        mbar_init(bar_mem + kYfree, kOutWarps);
-        mbar_init(bar_mem + kS, kOutWarps);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(bar_mem + kXw + i, kInWarps);
-            mbar_init(bar_mem + kDs + i, 1);
-            mbar_init(bar_mem + kDsFree + i, kOutWarps);
+        for (int i = 0; i < kBars; ++i) {
+            int count = 1;  // a commit, a copy or one warp
+            if ((i >= kEmpty && i < kEmpty + 4) || i == kS || i == kOut) count = kOutWarps;
+            if (i == kW || i == kC) count = kInWarps;
+            if (i == kXw || i == kXw + 1) count = OUT ? kInWarps : kWarps;
+            if (i == kDsFree || i == kDsFree + 1) count = kOutWarps / HALVES;
+            mbar_init(bar_mem + i, count);
         }
         abort_mem = 0;
         fence_mbar_init_cluster();
     }
-    if (warp == kWarps) tmem_alloc(&tmem_holder, 512);
+    if (warp == kMmaWarp) tmem_alloc(&tmem_holder, 512);
     if (OUT) {  // the blocks of W above its diagonal stay zero
         uint4* w = reinterpret_cast<uint4*>(sm + L.w_off);
         for (uint32_t i = threadIdx.x; i < HP * 1024u; i += kThreads) w[i] = make_uint4(0, 0, 0, 0);
@@ -152,106 +199,147 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
-    const uint32_t tm = tmem_holder;
+    constexpr uint32_t tm = 0;  // where an allocation of all 512 columns starts
 
-    const int q = warp & 3, part = (warp >> 2) & 1;                  // tensor-memory quadrant; half of the tokens or state columns
-    const uint32_t tq = tm + (static_cast<uint32_t>(q) << 21);      // this warp's 32 lanes
-    const int hw = HP == 4 ? q : HP == 2 ? q >> 1 : 0;              // head of its channels
-    // ldmatrix row of this lane in a block of 16 tokens x 16 channels (and stmatrix row in a patch of y)
+    const int q = warp & 3, part = (warp >> 2) & 1;             // tensor-memory quadrant; half of the tokens or state columns
+    const uint32_t tq = tm + (static_cast<uint32_t>(q) << 21);  // this warp's 32 lanes
+    const int hw = HP == 4 ? q : HP == 2 ? q >> 1 : 0;          // head of its channels
+    // ldmatrix row of this lane in a block of 16 tokens x 16 channels (and stmatrix row of a patch of y)
     const int row = 8 * (lane >> 4) + (lane & 7), pcol = 8 * ((lane >> 3) & 1);
-    uint32_t xaddr[2];  // channels q*32 + half*16.., tokens part*32..
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int pp = q * 32 + half * 16 + pcol;
-        xaddr[half] = s0 + (pp >> 6) * 8192 + (part * 32 + row) * 128 + ((((pp & 63) >> 3) ^ (row & 7)) << 4);
-    }
     auto done = [&](int i) {  // this warp's part of hand-over i
         tmem_fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive(bar(i));
     };
+    auto loaded = [&](int c, int st, uint32_t ph) {  // chunk c is in its stage
+        wait(kLanded + st, ph);
+        if (ragged && c == nch - 1) wait(kFixed, 0);
+    };
+    // Xw of 16 tokens (block `tb` of the chunk) and this warp's 32 channels, three exact pieces
+    auto weigh = [&](int i, int st, int tb) {
+        const uint32_t xw = tq + cXw + i * 96 + tb * 8;
+        const float* w = toks[st * HP + hw].w + tb * 16 + 2 * (lane & 3);
+        const float2 w0 = *reinterpret_cast<const float2*>(w), w1 = *reinterpret_cast<const float2*>(w + 8);
+        const F2 ww[2] = {f2(w0.x, w0.y), f2(w1.x, w1.y)};
+        uint32_t x[2][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int pp = q * 32 + half * 16 + pcol;
+            ldsm_t(s0 + st * L.stage_bytes + (pp >> 6) * 8192 + (tb * 16 + row) * 128 + ((((pp & 63) >> 3) ^ (row & 7)) << 4), x[half]);
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            uint32_t piece[3][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                F2 v = mul2(bf_pair(x[half][k]), ww[k >> 1]);
+                piece[0][k] = peel(v);
+                piece[1][k] = peel(v);
+                piece[2][k] = pack_cut(v);
+            }
+#pragma unroll
+            for (int s = 0; s < 3; ++s)
+                tmem_st_16x8(xw + (static_cast<uint32_t>(half) << 20) + s * 32, piece[s][0], piece[s][1], piece[s][2], piece[s][3]);
+        }
+    };
+    auto drain = [&](int i) {  // after an abort: tensor memory is given back only when nothing writes to it
+        if (*abort_flag && lane == 0) {
+            const uint64_t t_end = now_ns() + 2000000000ull;
+            mma_commit(bar(i));
+            for (uint32_t it = 0; it < kSpinLimit; ++it)
+                if (try_wait(bar(i), 0) || now_ns() > t_end) break;
+        }
+        __syncwarp();
+    };
 
     if (warp < kInWarps) {
-        // ------------------------------------------------------------ operands of the chunk: Xw, X^T and W
+        // ------------------------------------------------------------ operands of the chunk: Xw, C in 32 bits, W
         regs_down<kInRegs>();
         int st = 0;
         uint32_t ph = 0;
+        const int j = q * 16 + (lane >> 2);  // this lane's rows of W: tokens j and j + 8
         for (int c = 0; c < nch; ++c) {
-            const Tok* tok = toks + st * HP;
-            wait(kToks + st, ph);
-            wait(kLanded + st, ph);
-            if (r.last - r.first - c * kQ < kQ) wait(kFixed, 0);
-            const int i = NB == 2 ? c & 1 : 0;
-            // Xw's buffer: the product that read it is done
-            if (c >= NB) wait(kDs + i, NB == 2 ? ((c >> 1) - 1) & 1 : (c - 1) & 1);
-            tmem_fence_after_sync();
+            const ChunkTok* tok = toks + st * HP;
+            loaded(c, st, ph);
+            if constexpr (!OUT) {
+                if (c >= 2) wait(kDs + (c & 1), ((c >> 1) - 1) & 1);  // Xw's buffer: the product that read it is done
+                tmem_fence_after_sync();
+                weigh(c & 1, st, part);
+                tmem_wait_st();
+                done(kXw + (c & 1));
+            } else {
+                if (c > 0) wait(kDs + HALVES - 1, (c - 1) & 1);
+                tmem_fence_after_sync();
 #pragma unroll 1
-            for (int tg = 0; tg < 2; ++tg) {
-                const uint32_t xw = tq + cXw + i * 96 + part * 16 + tg * 8;
-                const float* w = tok[hw].w + part * 32 + tg * 16 + 2 * (lane & 3);
-                const float2 w0 = *reinterpret_cast<const float2*>(w), w1 = *reinterpret_cast<const float2*>(w + 8);
-                const F2 ww[2] = {f2(w0.x, w0.y), f2(w1.x, w1.y)};
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t xx[4];
-                    ldsm_t(xaddr[half] + st * L.stage_bytes + tg * 2048, xx);
-                    uint32_t piece[3][4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        F2 v = mul2(bf_pair(xx[k]), ww[k >> 1]);
-                        piece[0][k] = peel(v);
-                        piece[1][k] = peel(v);
-                        piece[2][k] = pack_cut(v);
-                    }
-#pragma unroll
-                    for (int s = 0; s < 3; ++s)
-                        tmem_st_16x8(xw + (static_cast<uint32_t>(half) << 20) + s * 32, piece[s][0], piece[s][1], piece[s][2], piece[s][3]);
+                for (int tg = 0; tg < 2; ++tg) weigh(0, st, part * 2 + tg);
+                tmem_wait_st();
+                done(kXw);
+                if (c > 0) wait(kY, (c - 1) & 1);  // the buffers of C and W: the products that read them are done
+                // C: 8 values per lane and step, 8 rows side by side
+#pragma unroll 1
+                for (int i = warp * 32 + lane; i < 64 * (N / 8); i += kInWarps * 32) {
+                    const int rr = ((i >> 3) / (N / 8)) * 8 + (i & 7), cc = (i >> 3) % (N / 8);  // token, 8 values
+                    const uint4 v = *reinterpret_cast<const uint4*>(sm + st * L.stage_bytes + L.c_off + (cc >> 3) * 8192 + rr * 128 +
+                                                                    (((cc & 7) ^ (rr & 7)) << 4));
+                    unsigned char* to = sm + L.c32_off + (cc >> 2) * 8192 + rr * 128;
+                    const int at = (cc & 3) * 2;
+                    *reinterpret_cast<float4*>(to + ((at ^ (rr & 7)) << 4)) = make_float4(bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y));
+                    *reinterpret_cast<float4*>(to + (((at + 1) ^ (rr & 7)) << 4)) = make_float4(bf_lo(v.z), bf_hi(v.z), bf_lo(v.w), bf_hi(v.w));
                 }
-            }
-            tmem_wait_st();
-            done(kXw + i);
-            if constexpr (OUT) {
+                fence_async_smem();
+                done(kC);
                 wait(kG, c & 1);
                 tmem_fence_after_sync();
-                // tokens j of block q reach tokens i of blocks q..3; this warp takes every second of them
+                // Tokens j of block q reach tokens i of blocks cb = q..3; the quadrant's two warps take every second cb.
 #pragma unroll 1
                 for (int cb = q + part; cb < 4; cb += 2) {
                     float gv[8];
-                    tmem_ld_16x16(tq + cYa + cb * 16, gv);
-                    const int j = q * 16 + (lane >> 2), i0 = cb * 16 + 2 * (lane & 3);
+                    tmem_ld_16x16(tq + cG + cb * 16, gv);
+                    const int i0 = cb * 16 + 2 * (lane & 3);
+                    const uint32_t wbuf = L.w_off + j * 128 + 4 * (lane & 3);
+                    const uint32_t at0 = wbuf + (((2 * cb) ^ (j & 7)) << 4), at1 = wbuf + (((2 * cb + 1) ^ (j & 7)) << 4);
+                    auto put = [&](int h, int rb, int k, F2 w) {
+                        const uint32_t at = (k ? at1 : at0) + h * 16384 + rb * 1024;
+                        *reinterpret_cast<uint32_t*>(sm + at) = peel(w);
+                        *reinterpret_cast<uint32_t*>(sm + at + 8192) = pack_rn(w);
+                    };
                     tmem_wait_ld();
                     settle(gv);
+                    if (cb != q) {
+                        // exp(a_i - a_j) d_j in three factors that meet at block ends, none above 1 in a decaying state
 #pragma unroll
-                    for (int h = 0; h < HP; ++h) {
-                        const Tok& tk = tok[h];
-                        const float skip = (p.D && head0 + h < hg) ? p.D[g * hg + head0 + h] : 0.0f;
-                        const uint32_t wbase = L.w_off + h * 16384 + j * 128 + (i0 & 7) * 2;
-                        F2 hi[2], lo[2];
+                        for (int h = 0; h < HP; ++h) {
+                            const ChunkTok& tk = tok[h];
+                            const float f = cb == q + 1 ? 1.0f : tk.blk[cb == q + 3 ? 2 : q];
+                            const float2 u0 = *reinterpret_cast<const float2*>(tk.u + i0), u1 = *reinterpret_cast<const float2*>(tk.u + i0 + 8);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float2 a = *reinterpret_cast<const float2*>(tk.hi + i0 + 8 * k);
-                            const float2 e = *reinterpret_cast<const float2*>(tk.lo + i0 + 8 * k);
-                            hi[k] = f2(a.x, a.y);
-                            lo[k] = f2(e.x, e.y);
+                            for (int rb = 0; rb < 2; ++rb) {
+                                const float v = tk.v[j + 8 * rb] * f;
+#pragma unroll
+                                for (int k = 0; k < 2; ++k)
+                                    put(h, rb, k, mul2(mul2(k ? f2(u1.x, u1.y) : f2(u0.x, u0.y), f2(v, v)),
+                                                       f2(gv[4 * k + 2 * rb], gv[4 * k + 2 * rb + 1])));
+                            }
                         }
+                    } else {
 #pragma unroll
-                        for (int rb = 0; rb < 2; ++rb) {
-                            const float4 tj = tk.t[j + 8 * rb];
+                        for (int h = 0; h < HP; ++h) {
+                            const ChunkTok& tk = tok[h];
+                            const float skip = (p.D && head0 + h < hg) ? p.D[g * hg + head0 + h] : 0.0f;
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                float u, v;
-                                un(add2(add2(hi[k], f2(-tj.x, -tj.x)), add2(lo[k], f2(-tj.y, -tj.y))), u, v);
-                                const F2 e = mul2(f2(ex2(u), ex2(v)), f2(tj.z, tj.z));
-                                F2 w = mul2(e, f2(gv[4 * k + 2 * rb], gv[4 * k + 2 * rb + 1]));
-                                if (cb == q) {
+                            for (int rb = 0; rb < 2; ++rb) {
+                                const float jh = tk.hi[j + 8 * rb], jl = tk.lo[j + 8 * rb], dj = tk.d[j + 8 * rb];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const float2 hi = *reinterpret_cast<const float2*>(tk.hi + i0 + 8 * k);
+                                    const float2 lo = *reinterpret_cast<const float2*>(tk.lo + i0 + 8 * k);
+                                    float u, v;
+                                    un(add2(add2(f2(hi.x, hi.y), f2(-jh, -jh)), add2(f2(lo.x, lo.y), f2(-jl, -jl))), u, v);
+                                    un(mul2(mul2(f2(ex2(u), ex2(v)), f2(dj, dj)), f2(gv[4 * k + 2 * rb], gv[4 * k + 2 * rb + 1])), u, v);
+                                    // nothing from later tokens; D x_i rides on the diagonal
                                     const int ii = i0 + 8 * k - (j + 8 * rb);
-                                    un(w, u, v);
-                                    // D x_i rides on the diagonal
-                                    w = f2(ii > 0 ? u : ii == 0 ? u + skip : 0.0f, ii > -1 ? v : ii == -1 ? v + skip : 0.0f);
+                                    put(h, rb, k, f2(ii > 0 ? u : ii == 0 ? u + skip : 0.0f, ii > -1 ? v : ii == -1 ? v + skip : 0.0f));
                                 }
-                                const uint32_t at = wbase + rb * 1024 + ((((i0 >> 3) + k) ^ (j & 7)) << 4);
-                                *reinterpret_cast<uint32_t*>(sm + at) = peel(w);
-                                *reinterpret_cast<uint32_t*>(sm + at + 8192) = pack_rn(w);
                             }
                         }
                     }
@@ -266,110 +354,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         regs_up<kOutRegs>();
         const int ch = c0 + q * 32 + lane;  // channel of this lane's state columns
         const bool mine = ch < cend;
-        const int64_t bh = static_cast<int64_t>(b) * p.H + g * hg + ch / p.P;
-        const int64_t np = static_cast<int64_t>(N) * p.P;
-        const int pc = ch % p.P;
-        constexpr int NC = N / 2;            // state columns per warp
+        const int64_t bh = static_cast<int64_t>(b) * p.H + g * hg + ch / P;
+        constexpr int64_t np = static_cast<int64_t>(N) * P;
+        constexpr int NC = N / 2;              // state columns per warp
         constexpr int NV = NC < 16 ? NC : 16;  // of them per tensor-memory access
+        const int64_t own = static_cast<int64_t>(part) * NC * P + ch % P;
         F2 S[NC / 2];
         {
             const float* from = nullptr;
             if (OUT && mine) {
-                if (p.split.nseg > 1) from = p.seg_state + (bh * p.split.slots() + seg * p.split.sub) * np;
-                else if (p.S_in) from = p.S_in + bh * np;
+                if (p.split.nseg > 1) from = p.seg_state + (bh * p.split.slots() + seg * p.split.sub) * np + own;
+                else if (p.S_in) from = p.S_in + bh * np + own;
             }
-            from = from ? from + static_cast<int64_t>(part) * NC * p.P + pc : nullptr;
 #pragma unroll
-            for (int k = 0; k < NC / 2; ++k) {
-                S[k] = from ? f2(from[0], from[p.P]) : f2(0.0f, 0.0f);
-                if (from) from += 2 * p.P;
-                if (k % 8 == 7) asm volatile("" ::: "memory");  // few loads, and few addresses, at a time
-            }
+            for (int k = 0; k < NC / 2; ++k) S[k] = from ? f2(from[2 * k * P], from[(2 * k + 1) * P]) : f2(0.0f, 0.0f);
         }
-        auto put_state = [&](int k0) {  // state columns k0 .. k0+NV as two pieces
-            uint32_t hi[NV / 2], lo[NV / 2];
+        auto put_state = [&]() {  // the state as an operand of Yb
 #pragma unroll
-            for (int k = 0; k < NV / 2; ++k) {
-                F2 v = S[k0 / 2 + k];
-                hi[k] = peel(v);
-                lo[k] = pack_rn(v);
+            for (int k0 = 0; k0 < NC; k0 += NV) {
+                uint32_t v[NV];
+#pragma unroll
+                for (int k = 0; k < NV / 2; ++k) {
+                    float a, e;
+                    un(S[k0 / 2 + k], a, e);
+                    v[2 * k] = __float_as_uint(a);
+                    v[2 * k + 1] = __float_as_uint(e);
+                }
+                tmem_st_cols<NV>(tq + cS + part * NC + k0, v);
             }
-            tmem_st_cols<NV / 2>(tq + cShi + (part * NC + k0) / 2, hi);
-            tmem_st_cols<NV / 2>(tq + cSlo + (part * NC + k0) / 2, lo);
-        };
-        if (OUT && nch > 0) {
-#pragma unroll
-            for (int k0 = 0; k0 < NC; k0 += NV) put_state(k0);
             tmem_wait_st();
             done(kS);
-        }
-        // this warp's patch of y: 32 tokens x 32 channels
-        const uint32_t patch = L.stg_off + (warp - kInWarps) * kPatch;
-        uint32_t paddr[2];  // stmatrix row of this lane, channels half*16..
-#pragma unroll
-        for (int half = 0; half < 2; ++half) paddr[half] = s0 + patch + row * 64 + (((half * 2 + (pcol >> 3)) ^ ((row >> 1) & 3)) << 4);
-        const bool ych = c0 + q * 32 < cend;
-        int st = 0;
-        uint32_t ph = 0;
-        for (int c = 0; c < nch; ++c) {
-            const Tok& tok = toks[st * HP + hw];
-            wait(kToks + st, ph);
-            if constexpr (OUT) {
-                if (lane == 0) store_read_done();  // the patch is free
-                __syncwarp();
-                wait(kY, c & 1);
-                tmem_fence_after_sync();
-                const uint32_t ty = tq + part * 32;
-                float yb[2][8], ya[2][8];
-                tmem_ld_16x16(ty + cYb, yb[0]);
-                tmem_ld_16x16(ty + cYa, ya[0]);
-#pragma unroll
-                for (int k4 = 0; k4 < 4; ++k4) {  // 16 tokens k4/2, 16 channels k4%2; the next loads run meanwhile
-                    const int now = k4 & 1, tg = k4 >> 1;
-                    const float* e = tok.ein + part * 32 + tg * 16 + 2 * (lane & 3);
-                    const float2 e0 = *reinterpret_cast<const float2*>(e), e1 = *reinterpret_cast<const float2*>(e + 8);
-                    tmem_wait_ld();
-                    settle(yb[now]);
-                    settle(ya[now]);
-                    if (k4 < 3) {
-                        const uint32_t at = ty + (static_cast<uint32_t>((k4 + 1) & 1) << 20) + ((k4 + 1) >> 1) * 16;
-                        tmem_ld_16x16(at + cYb, yb[now ^ 1]);
-                        tmem_ld_16x16(at + cYa, ya[now ^ 1]);
-                    } else {
-                        done(kYfree);
-                    }
-                    uint32_t o[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // 8 tokens k/2, 8 channels k%2
-                        const int at = 4 * (k >> 1) + 2 * (k & 1);
-                        const float2 ee = k < 2 ? e0 : e1;
-                        o[k] = pack_rn(fma2(f2(ee.x, ee.y), f2(yb[now][at], yb[now][at + 1]), f2(ya[now][at], ya[now][at + 1])));
-                    }
-                    stsm_t(paddr[k4 & 1] + tg * 1024, o[0], o[1], o[2], o[3]);
-                }
-                const int tok0 = r.first + c * kQ + part * 32, left = r.last - tok0;
-                if (left >= 32) {
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0 && ych) tma_store_3d(&maps.y, g * cend + c0 + q * 32, tok0, b, s0 + patch);
-                } else {  // rows behind the sequence are not this call's to write
-                    __syncwarp();
-                    const int64_t yrow = static_cast<int64_t>(p.H) * p.P;
-                    __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.T + tok0) * yrow + g * cend + c0 +
-                                        q * 32 + (lane & 3) * 8;
-#pragma unroll 1
-                    for (int t = lane >> 2; t < left && ych; t += 8)
-                        *reinterpret_cast<uint4*>(yp + t * yrow) =
-                            *reinterpret_cast<const uint4*>(sm + patch + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
-                    __syncwarp();
-                }
-            }
-            // S' = dec S + dS
-            const int i = NB == 2 ? c & 1 : 0;
-            wait(kDs + i, NB == 2 ? (c >> 1) & 1 : c & 1);
+        };
+        auto add_chunk = [&](int c, float decay) {  // S' = dec S + dS
+            const int i = OUT ? (HALVES == 2 ? part : 0) : c & 1;
+            wait(kDs + i, OUT ? c & 1 : (c >> 1) & 1);
             tmem_fence_after_sync();
-            const F2 dec = f2(tok.dec, tok.dec);
-            const uint32_t td = tq + cDs + i * 128 + part * NC;
+            const F2 dec = f2(decay, decay);
+            const uint32_t td = tq + cDs + (OUT ? 0 : i * 128) + (HALVES == 2 ? 0 : part * NC);
             float d[2][NV];
             tmem_ld_cols<NV>(td, d[0]);
 #pragma unroll
@@ -378,48 +399,114 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                 tmem_wait_ld();
                 settle(d[now]);
                 if (k0 + NV < NC) tmem_ld_cols<NV>(td + k0 + NV, d[now ^ 1]);
-                else done(kDsFree + i);  // the next chunk's dS may come while the state is split below
+                else done(kDsFree + i);
 #pragma unroll
                 for (int k = 0; k < NV / 2; ++k) S[k0 / 2 + k] = fma2(S[k0 / 2 + k], dec, f2(d[now][2 * k], d[now][2 * k + 1]));
             }
-            if (OUT && c + 1 < nch) {
+        };
+        if (OUT && nch > 0) put_state();
+        const uint32_t patch = L.patch_off + q * kPatch + part * (kPatch / 2);  // this warp's 32 tokens x 32 channels of y
+        int st = 0;
+        uint32_t ph = 0;
+        float before = 0.0f;  // the previous chunk's decay
+        for (int c = 0; c < nch; ++c) {
+            const ChunkTok& tok = toks[st * HP + hw];
+            loaded(c, st, ph);
+            const float decay = tok.dec;
+            if constexpr (OUT) {
+                // The state takes dS before the outputs are there, but for the second half where dS comes in halves
+                // (one copy of both parts, for the instruction cache).
+#pragma unroll 1
+                for (int step = 0; step < 2; ++step) {
+                    if (step == (HALVES == 2 ? part : 0)) {
+                        add_chunk(c, decay);
+                        continue;
+                    }
+                    if (c > 0) wait(kPatchFree, (c - 1) & 1);
+                    wait(kY, c & 1);
+                    tmem_fence_after_sync();
+                    const uint32_t ty = tq + part * 32;
+                    float yb[2][8], ya[2][8];
+                    tmem_ld_16x16(ty + cYb, yb[0]);
+                    tmem_ld_16x16(ty + cYa, ya[0]);
 #pragma unroll
-                for (int k0 = 0; k0 < NC; k0 += NV) put_state(k0);
-            }
-            if (OUT && c + 1 < nch) {
+                    for (int k4 = 0; k4 < 4; ++k4) {  // 16 tokens k4/2, 16 channels k4%2; the next loads run meanwhile
+                        const int now = k4 & 1, tg = k4 >> 1;
+                        const float* e = tok.ein + part * 32 + tg * 16 + 2 * (lane & 3);
+                        const float2 e0 = *reinterpret_cast<const float2*>(e), e1 = *reinterpret_cast<const float2*>(e + 8);
+                        tmem_wait_ld();
+                        settle(yb[now]);
+                        settle(ya[now]);
+                        if (k4 < 3) {
+                            const uint32_t at = ty + (static_cast<uint32_t>((k4 + 1) & 1) << 20) + ((k4 + 1) >> 1) * 16;
+                            tmem_ld_16x16(at + cYb, yb[now ^ 1]);
+                            tmem_ld_16x16(at + cYa, ya[now ^ 1]);
+                        }
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {  // 8 tokens k/2, 8 channels k%2
+                            const int at = 4 * (k >> 1) + 2 * (k & 1);
+                            const float2 ee = k < 2 ? e0 : e1;
+                            o[k] = pack_rn(fma2(f2(ee.x, ee.y), f2(yb[now][at], yb[now][at + 1]), f2(ya[now][at], ya[now][at + 1])));
+                        }
+                        stsm_t(s0 + patch + (tg * 16 + row) * 64 + ((((k4 & 1) * 2 + (pcol >> 3)) ^ ((row >> 1) & 3)) << 4), o[0], o[1], o[2], o[3]);
+                    }
+                    fence_async_smem();
+                }
+                if (c + 1 < nch) put_state();
+                done(kOut);  // (with the fence above: the patch is complete for the store)
+                if (ragged && c == nch - 1) {  // rows behind the sequence are not this call's to write
+                    const int tok0 = r.first + c * kQ + part * 32, left = r.last - tok0;
+                    const int64_t yrow = static_cast<int64_t>(p.H) * P;
+                    __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.T + tok0) * yrow + g * cend + c0 +
+                                        q * 32 + (lane & 3) * 8;
+#pragma unroll 1
+                    for (int t = lane >> 2; t < min(left, 32) && c0 + q * 32 < cend; t += 8)
+                        *reinterpret_cast<uint4*>(yp + t * yrow) =
+                            *reinterpret_cast<const uint4*>(sm + patch + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+                }
+                __syncwarp();
+                if (lane == 0) arrive(bar(kEmpty + st));
+            } else {
+                if (c >= 2) wait(kDs + (c & 1), ((c >> 1) - 1) & 1);
+                tmem_fence_after_sync();
+                weigh(c & 1, st, 2 + part);
                 tmem_wait_st();
-                done(kS);
+                done(kXw + (c & 1));
+                if (c > 0) {
+                    add_chunk(c - 1, before);
+                    __syncwarp();
+                    if (lane == 0) arrive(bar(kEmpty + (st == 0 ? L.stages - 1 : st - 1)));
+                }
+                before = decay;
             }
-            __syncwarp();
-            if (lane == 0) arrive(bar(kEmpty + st));
             if (++st == L.stages) st = 0, ph ^= 1;
         }
-        if (OUT && lane == 0) store_done();
+        if (!OUT && nch > 0) add_chunk(nch - 1, before);
         float* to = nullptr;
         if (mine) {
-            if (!OUT) to = p.seg_state + (bh * p.split.slots() + seg) * np;
-            else if (seg == p.split.nseg - 1) to = p.S_out + bh * np;
+            if (!OUT) to = p.seg_state + (bh * p.split.slots() + seg) * np + own;
+            else if (seg == p.split.nseg - 1) to = p.S_out + bh * np + own;
         }
         if (to) {
-            to += static_cast<int64_t>(part) * NC * p.P + pc;
 #pragma unroll
-            for (int k = 0; k < NC / 2; ++k) {
-                un(S[k], to[0], to[p.P]);
-                to += 2 * p.P;
-            }
+            for (int k = 0; k < NC / 2; ++k) un(S[k], to[2 * k * P], to[(2 * k + 1) * P]);
         }
-    } else if (warp == kWarps) {
+    } else if (warp == kLoadWarp) {
         // ------------------------------------------------------------ TMA
         regs_down<kMiscRegs>();
+        const int heads = min(HP, hg - head0);
+        const int chunks = (p.T + kQ - 1) / kQ;
+        const ChunkTok* src = p.toks + (static_cast<int64_t>(b) * p.H + g * hg + head0) * chunks + r.first / kQ;
         int issued = 0;
-        for (int c = 0; c < nch; ++c) {
-            const int st = c % L.stages;
-            if (c >= L.stages) wait(kEmpty + st, ((c / L.stages) - 1) & 1);
-            if (*abort_flag) break;
-            const int t0 = r.first + c * kQ, nv = min(kQ, r.last - t0);
+        auto load = [&](int c) {
+            const int st = c % L.stages, t0 = r.first + c * kQ, nv = min(kQ, r.last - t0);
             const uint32_t base = s0 + st * L.stage_bytes;
             if (lane == 0) {
-                arrive_tx(bar(kLanded + st), L.stage_bytes);
+                arrive_tx(bar(kLanded + st), L.stage_bytes + heads * static_cast<uint32_t>(sizeof(ChunkTok)));
+                for (int h = 0; h < heads; ++h)
+                    bulk_load(s0 + L.tok_off + (st * HP + h) * static_cast<uint32_t>(sizeof(ChunkTok)), src + static_cast<int64_t>(h) * chunks + c,
+                              sizeof(ChunkTok), bar(kLanded + st));
                 tma_load_3d(base, &maps.x, g * cend + c0, t0, b, bar(kLanded + st));
                 tma_load_3d(base + 8192, &maps.x, g * cend + c0 + 64, t0, b, bar(kLanded + st));
 #pragma unroll
@@ -438,7 +525,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                 __syncwarp();
                 if (lane == 0) arrive(bar(kFixed));
             }
+        };
+#pragma unroll 1
+        for (int c = -L.stages; c < nch && !*abort_flag; ++c) {  // the first rounds only load
+            bool stored = false;
+            if (OUT && c >= 0) {
+                wait(kOut, c & 1);
+                stored = !(ragged && c == nch - 1);
+                if (stored && lane == 0)
+                    for (int k = 0; k < 4; ++k)
+                        if (c0 + k * 32 < cend)
+                            tma_store_3d(&maps.y, g * cend + c0 + k * 32, r.first + c * kQ, b, s0 + L.patch_off + k * kPatch);
+            }
+            if (c + L.stages < nch) {
+                if (c >= 0) wait(kEmpty + c % L.stages, (c / L.stages) & 1);
+                if (!*abort_flag) load(c + L.stages);
+            }
+            if (stored) {
+                if (lane == 0) {
+                    store_read_done();
+                    arrive(bar(kPatchFree));
+                }
+                __syncwarp();
+            }
         }
+        if (OUT && lane == 0) store_done();
         // no copy may land in this block's memory after it has gone (bounded, also after an abort)
         if (*abort_flag && lane == 0) {
             const uint64_t t_end = now_ns() + 2000000000ull;
@@ -446,58 +557,75 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                 for (uint32_t it = 0; it < kSpinLimit; ++it)
                     if (try_wait(bar(kLanded + c % L.stages), (c / L.stages) & 1) || now_ns() > t_end) break;
         }
-    } else if (warp == kWarps + 1) {
-        // ------------------------------------------------------------ MMA issue (whole warp, one lane issues)
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issue: G and dS (whole warp, one lane issues)
         regs_down<kMiscRegs>();
-        constexpr uint32_t wG = mma_word(64, 64, false, false), wYb = mma_word(128, 64, false, false);
-        constexpr uint32_t wYa = mma_word(128, 64, true, true), wDs = mma_word(128, N, false, true);
-        const Desc wdesc = desc_of(s0 + L.w_off, 8192);
-        auto add_chunk = [&](int c, int st) {  // dS of chunk c
-            const Desc down = desc_of(s0 + st * L.stage_bytes + L.b_off, 8192);  // B as [j, n]: contraction down the rows
-            const int i = NB == 2 ? c & 1 : 0;
-            wait(kXw + i, NB == 2 ? (c >> 1) & 1 : c & 1);
-            if (c >= NB) wait(kDsFree + i, NB == 2 ? ((c >> 1) - 1) & 1 : (c - 1) & 1);
+        constexpr int ND = HALVES == 2 ? 64 : N;  // columns of one dS product
+        constexpr uint32_t wG = mma_word(64, 64, false, false), wDs = mma_word(128, ND, false, true);
+        auto issue_g = [&](int st) {
+            const Desc along = desc_of(s0 + st * L.stage_bytes, 16);  // B and C as [token, n]: contraction along the rows
+            tmem_fence_after_sync();
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < N / 16; ++k)
+                    mma_ss(tm + cG, along + (L.b_off + (k >> 2) * 8192 + (k & 3) * 32), along + (L.c_off + (k >> 2) * 8192 + (k & 3) * 32), wG,
+                           k > 0);
+                mma_commit(bar(kG));
+            }
+            __syncwarp();
+        };
+        auto issue_ds = [&](int i, int xb, int half, int st) {  // a part of dS, signalled on kDs + i
+            const Desc down = desc_of(s0 + st * L.stage_bytes + L.b_off + half * 8192, 8192);  // B as [j, n]: contraction down the rows
             tmem_fence_after_sync();
             if (elect_one()) {
 #pragma unroll
                 for (int s = 2; s >= 0; --s)  // the small pieces first
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ts(tm + cDs + i * 128, tm + cXw + i * 96 + s * 32 + k * 8, down + k * 2048, wDs, s < 2 || k > 0);
+                        mma_ts(tm + cDs + (OUT ? 0 : i * 128), tm + cXw + xb * 96 + s * 32 + k * 8, down + k * 2048, wDs, s < 2 || k > 0);
                 mma_commit(bar(kDs + i));
             }
             __syncwarp();
         };
         int st = 0;
         uint32_t ph = 0;
-        for (int c = 0; c < nch; ++c) {
-            const Desc down = desc_of(s0 + st * L.stage_bytes, 8192);  // x as [j, p]: contraction down the rows
-            const Desc along = desc_of(s0 + st * L.stage_bytes, 16);   // contraction along the rows: B and C as [., n]
-            wait(kLanded + st, ph);
-            if (r.last - r.first - c * kQ < kQ) wait(kFixed, 0);
-            if (*abort_flag) break;
+        for (int c = 0; c < nch && !*abort_flag; ++c) {
+            loaded(c, st, ph);
             if constexpr (OUT) {
-                if (c > 0) wait(kYfree, (c - 1) & 1);
-                tmem_fence_after_sync();
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < N / 16; ++k)
-                        mma_ss(tm + cYa, along + (L.b_off + (k >> 2) * 8192 + (k & 3) * 32), along + (L.c_off + (k >> 2) * 8192 + (k & 3) * 32),
-                               wG, k > 0);
-                    mma_commit(bar(kG));
+                if (c > 0) wait(kW, (c - 1) & 1);  // G's columns have been read
+                issue_g(st);
+                wait(kXw, c & 1);
+                if (c > 0) wait(kDsFree + HALVES - 1, (c - 1) & 1);
+#pragma unroll 1
+                for (int half = 0; half < HALVES; ++half) {
+                    if (half == 1) wait(kDsFree, c & 1);
+                    issue_ds(half, 0, half, st);
                 }
-                __syncwarp();
+            } else {
+                wait(kXw + (c & 1), (c >> 1) & 1);
+                if (c >= 2) wait(kDsFree + (c & 1), ((c >> 1) - 1) & 1);
+                issue_ds(c & 1, c & 1, 0, st);
             }
-            if constexpr (OUT) {
-                add_chunk(c, st);
-                wait(kS, c & 1);
+            if (++st == L.stages) st = 0, ph ^= 1;
+        }
+        drain(kDrain);
+    } else if (warp == kMmaWarp + 1) {
+        // ------------------------------------------------------------ MMA issue: Yb and Ya
+        regs_down<kMiscRegs>();
+        if constexpr (OUT) {
+            constexpr uint32_t wYb = mma_word_tf32(128, 64), wYa = mma_word(128, 64, true, true);
+            const Desc along = desc_of(s0 + L.c32_off, 16);  // C as [i, n]: contraction along the rows
+            const Desc wd = desc_of(s0 + L.w_off, 8192);
+            int st = 0;
+            for (int c = 0; c < nch && !*abort_flag; ++c) {
+                const Desc down = desc_of(s0 + st * L.stage_bytes, 8192);  // x as [j, p]: contraction down the rows
+                wait(kC, c & 1);  // C is there, and with it x
+                wait(kS, c & 1);  // the state is there, and the columns of Ya and Yb have been read
                 tmem_fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
-                    for (int s = 0; s < 2; ++s)
-#pragma unroll
-                        for (int k = 0; k < N / 16; ++k)
-                            mma_ts(tm + cYb, tm + (s ? cShi : cSlo) + k * 8, along + (L.c_off + (k >> 2) * 8192 + (k & 3) * 32), wYb, s + k > 0);
+                    for (int k = 0; k < N / 8; ++k)
+                        mma_ts_tf32(tm + cYb, tm + cS + k * 8, along + ((k >> 2) * 8192 + (k & 3) * 32), wYb, k > 0);
                 }
                 __syncwarp();
                 wait(kW, c & 1);
@@ -509,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                         for (int s = 0; s < 2; ++s)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const Desc da = down + k * 2048, db = wdesc + (h * 16384 + (s ? 0 : 8192) + k * 2048);
+                                const Desc da = down + k * 2048, db = wd + (h * 16384 + (s ? 0 : 8192) + k * 2048);
                                 if constexpr (HP == 1) {
                                     mma_ss(tm + cYa, da, db, wYa, s + k > 0);
                                 } else {
@@ -520,93 +648,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     mma_commit(bar(kY));
                 }
                 __syncwarp();
+                if (++st == L.stages) st = 0;
             }
-            if constexpr (!OUT) add_chunk(c, st);
-            if (++st == L.stages) st = 0, ph ^= 1;
+            drain(kDrain + 1);
         }
-        if (*abort_flag && lane == 0) {  // tensor memory is given back only when nothing writes to it
-            const uint64_t t_end = now_ns() + 2000000000ull;
-            mma_commit(bar(kDrain));
-            for (uint32_t it = 0; it < kSpinLimit; ++it)
-                if (try_wait(bar(kDrain), 0) || now_ns() > t_end) break;
-        }
-        __syncwarp();
     } else {
-        // ------------------------------------------------------------ step sizes and decays
-        regs_down<kMiscRegs>();
-        const int first = warp - (kWarps + 2);
-        const __nv_bfloat16* dt = reinterpret_cast<const __nv_bfloat16*>(p.dt) + b * p.dts.b + (g * hg + head0) * p.dts.h;
-        if (!OUT && lane < HP) log_mem[first][lane] = 0.0;
-        __syncwarp();
-        uint32_t raw_dt[2];  // the step inputs of the next (chunk, head), loaded one ahead
-        auto fetch = [&](int c, int h) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int t = r.first + c * kQ + 2 * lane + k;
-                raw_dt[k] = (c < nch && head0 + h < hg && t < r.last) ? __bfloat16_as_ushort(dt[t * p.dts.t + h * p.dts.h]) : 0u;
-            }
-        };
-        fetch(first, 0);
-#pragma unroll 1
-        for (int c = first; c < nch; c += kDtWarps) {
-            const int st = c % L.stages;
-            if (c >= L.stages) wait(kEmpty + st, ((c / L.stages) - 1) & 1);
-            if (*abort_flag) break;
-#pragma unroll 1
-            for (int h = 0; h < HP; ++h) {
-                const bool real = head0 + h < hg;
-                const double A = real ? static_cast<double>(p.A[g * hg + head0 + h]) : 0.0;
-                const float bias = (real && p.dt_bias) ? p.dt_bias[g * hg + head0 + h] : 0.0f;
-                float d[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k)  // a token that is not there neither decays nor writes
-                    d[k] = (real && r.first + c * kQ + 2 * lane + k < r.last)
-                               ? step_size(__uint_as_float(raw_dt[k] << 16), bias, p.softplus, p.dt_min, p.dt_max)
-                               : 0.0f;
-                if (h + 1 < HP) fetch(c, h + 1);
-                else fetch(c + kDtWarps, 0);
-                const double a0 = d[0] * A, a1 = d[1] * A;
-                double sum = a0 + a1;
-#pragma unroll 1
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double up = __shfl_up_sync(0xffffffffu, sum, o);
-                    if (lane >= o) sum += up;
-                }
-                const double total = __shfl_sync(0xffffffffu, sum, 31);
-                Tok& tk = toks[st * HP + h];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const double cum = k ? sum : sum - a1;
-                    const double l2 = cum * 1.4426950408889634074;
-                    const float hi = static_cast<float>(l2), lo = static_cast<float>(l2 - static_cast<double>(hi));
-                    const float w = d[k] * expf(static_cast<float>(total - cum));
-                    const int j = 2 * lane + k;
-                    tk.t[j] = make_float4(hi, lo, d[k], w);
-                    tk.hi[j] = hi;
-                    tk.lo[j] = lo;
-                    tk.ein[j] = expf(static_cast<float>(cum));
-                    tk.w[j] = w;
-                }
-                const float dec = static_cast<float>(exp(total));
-                if (lane == 0) {
-                    tk.dec = dec;
-                    if (!OUT) log_mem[first][h] += total;
-                }
-            }
-            __syncwarp();
-            if (lane == 0) arrive(bar(kToks + st));
-        }
+        regs_down<kMiscRegs>();  // the warp that makes up the group
     }
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
-    if (warp == kWarps) tmem_dealloc(tm, 512);
+    if (warp == kMmaWarp) tmem_dealloc(tm, 512);
     if (threadIdx.x == 0 && *abort_flag) set_status(p.status, kDevTimeout);
-    if (!OUT && threadIdx.x < HP && head0 + static_cast<int>(threadIdx.x) < hg && c0 % p.P == 0) {
-        double sum = 0.0;
-        for (int k = 0; k < kDtWarps; ++k) sum += log_mem[k][threadIdx.x];
-        p.seg_decay[(static_cast<int64_t>(b) * p.H + g * hg + head0 + threadIdx.x) * p.split.pieces() + seg] = static_cast<float>(exp(sum));
-    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -648,40 +701,43 @@ bool map_operands(const SsmParams& p, MmaMaps* m)
     const int64_t xsize[3] = {static_cast<int64_t>(p.H) * p.P, p.T, p.B}, xstr[3] = {1, p.xs.t, p.xs.b};
     const int64_t bsize[4] = {p.N, p.G, p.T, p.B}, bstr[4] = {1, p.bs.h, p.bs.t, p.bs.b}, cstr[4] = {1, p.cs.h, p.cs.t, p.cs.b};
     const int64_t ystr[3] = {1, xsize[0], xsize[0] * p.T};
-    return encode(&m->y, p.y, 3, xsize, ystr, 32, 32) && encode(&m->x, p.x, 3, xsize, xstr) && encode(&m->b, p.Bm, 4, bsize, bstr) && encode(&m->c, p.Cm, 4, bsize, cstr);
+    return encode(&m->y, p.y, 3, xsize, ystr, 32, 64) && encode(&m->x, p.x, 3, xsize, xstr) && encode(&m->b, p.Bm, 4, bsize, bstr) && encode(&m->c, p.Cm, 4, bsize, cstr);
 }
 
-template <int N, int HP, bool OUT>
+template <int N, int P, bool OUT>
 cudaError_t go(const SsmParams& p, const MmaMaps& m, int tiles, int segs, cudaStream_t s)
 {
-    constexpr Layout L = layout_of(N, HP, OUT);
+    constexpr Layout L = layout_of(N, P >= 128 ? 1 : 128 / P, OUT);
     static_assert(kThreads == 640, "register split");
     static_assert(L.total <= kSmemMax, "shared memory");
-    auto kern = k_ssm_mma<N, HP, OUT>;
+    auto kern = k_ssm_mma<N, P, OUT>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L.total));
     if (e != cudaSuccess) return e;
     kern<<<dim3(static_cast<unsigned>(p.B) * p.G * tiles, segs), kThreads, L.total, s>>>(m, p, tiles);
     return cudaGetLastError();
 }
 
-template <int N, int HP>
+template <int N, int P>
 cudaError_t all(const SsmParams& p, const MmaMaps& m, cudaStream_t s)
 {
     const int tiles = (p.H / p.G * p.P + 127) / 128;
     if (p.split.nseg > 1) {
-        cudaError_t e = go<N, HP, false>(p, m, tiles, p.split.pieces(), s);
+        cudaError_t e = go<N, P, false>(p, m, tiles, p.split.pieces(), s);
         if (e == cudaSuccess) e = launch_ssm_chain(p, s);
         if (e != cudaSuccess) return e;
     }
-    return go<N, HP, true>(p, m, tiles, p.split.nseg, s);
+    return go<N, P, true>(p, m, tiles, p.split.nseg, s);
 }
 
 template <int N>
 cudaError_t pick(const SsmParams& p, const MmaMaps& m, cudaStream_t s)
 {
-    if (p.P == 32) return all<N, 4>(p, m, s);
-    if (p.P == 64) return all<N, 2>(p, m, s);
-    return all<N, 1>(p, m, s);
+    switch (p.P) {
+        case 32: return all<N, 32>(p, m, s);
+        case 64: return all<N, 64>(p, m, s);
+        case 128: return all<N, 128>(p, m, s);
+        default: return all<N, 256>(p, m, s);
+    }
 }
 
 bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -705,6 +761,11 @@ cudaError_t launch_ssm_mma(const SsmParams& p, cudaStream_t s)
 {
     MmaMaps m;
     if (!map_operands(p, &m)) return cudaErrorInvalidValue;
+    const int chunks = (p.T + kQ - 1) / kQ;
+    const int64_t work = static_cast<int64_t>(p.B) * p.H * chunks;
+    k_ssm_decay<<<static_cast<unsigned>((work + 7) / 8), 256, 0, s>>>(p, chunks, work);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     switch (p.N) {
         case 16: return pick<16>(p, m, s);
         case 32: return pick<32>(p, m, s);

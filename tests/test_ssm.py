@@ -2,9 +2,10 @@
 
 Tolerances are bounds, element by element:
   - fp32 roundings of the scan: the bound the oracle carries along with the recurrence;
-  - prompts with bf16 inputs and output may hold the state and the token-to-token weights as two bf16
-    pieces (16 bits or more of each value, 2^-16 relative) where they meet bf16 operands, and sum up to 64
-    tokens at once: 2^-15 of the sum of absolute values for both and the order of the sums;
+  - prompts with bf16 inputs and output meet the state as a tensor-core operand of 11 bits (tf32 cuts an fp32
+    value off behind 10 bits of fraction: at most 2^-10 of it) and the token-to-token weights as two bf16 pieces
+    (2^-16), and sum up to 64 tokens at once (64 u, 2^-18): together at most 2^-10 + 2^-15 of the sum of absolute
+    values;
   - one rounding to the output's type: half a step, eps / 2 of the value.
 """
 import numpy as np
@@ -55,7 +56,7 @@ def _layer(B, T, H, G, N, P, dtype, seed=0, dt_hi=0.1):
 
 
 def _scan_tols(y, ya, ye, E, S, out_dtype, split, Sa_bound=None):
-    ty = ye + _half_step(y, out_dtype) + (2.0 ** -15 * ya if split else 0)
+    ty = ye + _half_step(y, out_dtype) + ((2.0 ** -10 + 2.0 ** -15) * ya if split else 0)
     # blocks of 64 tokens are summed at once: 64 more roundings than token by token
     tS = E + (64 * U32 * S.abs().amax(dim=(2, 3), keepdim=True) if split else 0) + 1e-30
     return ty, tS
