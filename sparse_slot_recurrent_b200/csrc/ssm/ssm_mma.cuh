@@ -115,10 +115,11 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo)
 }
 
 // Instruction word: bf16 x bf16 -> fp32, M x N; ta / tb: the operand's contraction runs down the
-// rows of shared memory (its other dimension is contiguous).
-__host__ __device__ constexpr uint32_t mma_word(int M, int N, bool ta, bool tb)
+// rows of shared memory (its other dimension is contiguous); na / nb: the operand is taken negated.
+__host__ __device__ constexpr uint32_t mma_word(int M, int N, bool ta, bool tb, bool na = false, bool nb = false)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(ta) << 15) | (static_cast<uint32_t>(tb) << 16) |
+    return (static_cast<uint32_t>(na) << 13) | (static_cast<uint32_t>(nb) << 14) |
+           (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(ta) << 15) | (static_cast<uint32_t>(tb) << 16) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
@@ -153,27 +154,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, Desc b, uint32_t 
 }
 
 // ... leaving alone the tensor-memory lanes whose bit is set in m0 (lanes 0..31) .. m3 (96..127)
-__device__ __forceinline__ void mma_ss_masked(uint32_t d, Desc a, Desc b, uint32_t word, uint32_t m0, uint32_t m1, uint32_t m2, uint32_t m3,
-                                              bool add)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, {%7, %8, %9, %10}, p;\n\t}" ::"r"(d),
-        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(m0), "r"(m1), "r"(m2), "r"(m3)
-        : "memory");
-}
-
-// ... with both operands fp32 taken as tf32 (10 bits behind the leading one, the rest cut off)
-__host__ __device__ constexpr uint32_t mma_word_tf32(int M, int N)
-{
-    return (1u << 4) | (2u << 7) | (2u << 10) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-__device__ __forceinline__ void mma_ts_tf32(uint32_t d, uint32_t a, Desc b, uint32_t word, bool add)
+__device__ __forceinline__ void mma_ts_masked(uint32_t d, uint32_t a, Desc b, uint32_t word, uint32_t m0, uint32_t m1, uint32_t m2,
+                                              uint32_t m3, bool add)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.u32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add))
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, {%6, %7, %8, %9}, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b.lo), "r"(b.hi), "r"(word), "r"(static_cast<uint32_t>(add)), "r"(m0), "r"(m1), "r"(m2), "r"(m3)
         : "memory");
 }
 
@@ -337,14 +324,17 @@ __device__ __forceinline__ uint32_t pack_cut(F2 p)  // the leading 8 bits of bot
     un(p, a, b);
     return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-// The leading 8 bits of both as one pair of bf16; p keeps what is left (exact).
+// The leading 8 bits of both as one pair of bf16; p keeps what is left, negated (exact).  The differences take the
+// bf16 halves as they are, on the multiply-add pipe: the integer pipe has enough to do (a split that masks and
+// subtracts in 32 bits measured 7.4 issue cycles per pair, this one 4.8).
 __device__ __forceinline__ uint32_t peel(F2& p)
 {
     float a, b;
     un(p, a, b);
-    const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
-    p = add2(p, f2(__uint_as_float((ua & 0xffff0000u) ^ 0x80000000u), __uint_as_float((ub & 0xffff0000u) ^ 0x80000000u)));
-    return __byte_perm(ua, ub, 0x7632);
+    const uint32_t h = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tsub.rn.f32.bf16 %0, x, %0;\n\tsub.rn.f32.bf16 %1, y, %1;\n\t}" : "+f"(a), "+f"(b) : "r"(h));
+    p = f2(a, b);
+    return h;
 }
 
 }  // namespace

@@ -120,15 +120,17 @@ __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
     const int e = blockIdx.x * 256 + threadIdx.x;
     const int64_t bh = blockIdx.y;
     const int n = p.split.pieces(), sub = p.split.sub;
-    for (int k = threadIdx.x; k < n; k += 256) {
+    for (int k = threadIdx.x >> 5; k < n; k += 8) {  // a warp per piece
         if (p.toks) {
             const int chunks = (p.T + kChunk - 1) / kChunk, per = p.split.piece_len() / kChunk;
             const int b = static_cast<int>((bh + p.chain_first) / p.H);
             const int have = (seq_len(p.lengths, b, p.T) + kChunk - 1) / kChunk;  // chunks that the sequence has
             double sum = 0.0;
-            for (int i = k * per; i < min((k + 1) * per, have); ++i) sum += p.toks[bh * chunks + i].total;
-            decay[k] = exp2_of(sum);
-        } else {
+            for (int i = k * per + (threadIdx.x & 31); i < min((k + 1) * per, have); i += 32) sum += p.toks[bh * chunks + i].total;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if ((threadIdx.x & 31) == 0) decay[k] = exp2_of(sum);
+        } else if ((threadIdx.x & 31) == 0) {
             decay[k] = p.seg_decay[bh * n + k];
         }
     }

@@ -43,14 +43,17 @@ constexpr int kThreads = 20 * 32;
 constexpr uint32_t kPatch = 4096;  // y of 64 tokens x 32 channels, rows of 64 bytes in the 64-byte swizzle
 constexpr size_t kSmemMax = 232448 - 1024;  // the rest: barriers
 
-// Hand-overs.  Without outputs two chunks are in flight and alternate between two barriers of a kind; elsewhere
-// each side of a hand-over waits for the other before the next, so no waiting warp is ever a phase behind.
-enum Bar { kLanded = 0, kEmpty = 4, kFixed = 8, kG, kW, kC, kY, kS, kOut, kPatchFree, kXw, kDs = kXw + 2, kDsFree = kDs + 2,
+// Hand-overs.  Where a side may run two chunks ahead of the other, chunks alternate between two barriers of a kind;
+// elsewhere each side waits for the other before its next, so no waiting warp is ever more than a phase behind.
+enum Bar { kLanded = 0, kEmpty = 4, kFixed = 8, kG, kW, kY, kYfree, kS, kOut, kPatchFree = kOut + 2, kXw = kPatchFree + 2, kDs = kXw + 2, kDsFree = kDs + 2,
            kDrain = kDsFree + 2, kBars = kDrain + 2 };
+
+// Buffers of W and of the patch of y: two for one head per 128 channels; with more, the memory goes to W itself.
+__host__ __device__ constexpr int buffers(int HP) { return HP == 1 ? 2 : 1; }
 
 struct Layout {
     int stages;
-    uint32_t b_off, c_off, stage_bytes, w_off, c32_off, patch_off, tok_off, total;
+    uint32_t b_off, c_off, stage_bytes, w_off, patch_off, tok_off, total;
 };
 
 __host__ __device__ constexpr Layout layout_of(int N, int HP, bool out)
@@ -60,13 +63,12 @@ __host__ __device__ constexpr Layout layout_of(int N, int HP, bool out)
     l.b_off = 16384;
     l.c_off = l.b_off + nt;
     l.stage_bytes = l.c_off + (out ? nt : 0);
-    const uint32_t w = out ? HP * 16384u : 0, c32 = out ? (N + 31) / 32 * 8192u : 0, patch = out ? 4 * kPatch : 0;
+    const uint32_t w = out ? buffers(HP) * HP * 16384u : 0, patch = out ? buffers(HP) * 4 * kPatch : 0;
     const uint32_t tok = HP * static_cast<uint32_t>(sizeof(ChunkTok));
     l.stages = 4;
-    while (l.stages > 2 && l.stages * (l.stage_bytes + tok) + w + c32 + patch + 1024 > kSmemMax) --l.stages;
+    while (l.stages > 2 && l.stages * (l.stage_bytes + tok) + w + patch + 1024 > kSmemMax) --l.stages;
     l.w_off = l.stages * l.stage_bytes;
-    l.c32_off = l.w_off + w;
-    l.patch_off = l.c32_off + c32;
+    l.patch_off = l.w_off + w;
     l.tok_off = l.patch_off + patch;
     l.total = l.tok_off + l.stages * tok + 1024;  // 1024: base alignment
     return l;
@@ -151,9 +153,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
 {
     constexpr int HP = P >= 128 ? 1 : 128 / P;
     constexpr Layout L = layout_of(N, HP, OUT);
+    constexpr int NBUF = buffers(HP);
     constexpr int HALVES = OUT && N == 128 ? 2 : 1;  // dS comes in halves of 64 columns where tensor memory is short
     // tensor-memory columns
-    constexpr uint32_t cDs = 0, cS = 64, cXw = OUT ? 192 : 256, cYb = 288, cYa = 352, cG = 416;
+    constexpr uint32_t cDs = 0, cShi = 64, cSlo = 128, cXw = OUT ? 192 : 256, cX = 288, cYb = 320, cYa = 384, cG = 448;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bar_mem[kBars];
     __shared__ uint32_t tmem_holder;
@@ -181,9 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
             int count = 1;  // a commit, a copy or one warp
-            if ((i >= kEmpty && i < kEmpty + 4) || i == kS || i == kOut) count = kOutWarps;
-            if (i == kW || i == kC) count = kInWarps;
-            if (i == kXw || i == kXw + 1) count = OUT ? kInWarps : kWarps;
+            if ((i >= kEmpty && i < kEmpty + 4) || i == kS || i == kYfree || i == kOut || i == kOut + 1) count = kOutWarps;
+            if (i == kW || i == kXw || i == kXw + 1) count = kInWarps;
             if (i == kDsFree || i == kDsFree + 1) count = kOutWarps / HALVES;
             mbar_init(bar_mem + i, count);
         }
@@ -193,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     if (warp == kMmaWarp) tmem_alloc(&tmem_holder, 512);
     if (OUT) {  // the blocks of W above its diagonal stay zero
         uint4* w = reinterpret_cast<uint4*>(sm + L.w_off);
-        for (uint32_t i = threadIdx.x; i < HP * 1024u; i += kThreads) w[i] = make_uint4(0, 0, 0, 0);
+        for (uint32_t i = threadIdx.x; i < NBUF * HP * 1024u; i += kThreads) w[i] = make_uint4(0, 0, 0, 0);
         fence_async_smem();
     }
     tmem_fence_before_sync();
@@ -215,18 +217,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         wait(kLanded + st, ph);
         if (ragged && c == nch - 1) wait(kFixed, 0);
     };
-    // Xw of 16 tokens (block `tb` of the chunk) and this warp's 32 channels, three exact pieces
-    auto weigh = [&](int i, int st, int tb) {
-        const uint32_t xw = tq + cXw + i * 96 + tb * 8;
-        const float* w = toks[st * HP + hw].w + tb * 16 + 2 * (lane & 3);
-        const float2 w0 = *reinterpret_cast<const float2*>(w), w1 = *reinterpret_cast<const float2*>(w + 8);
-        const F2 ww[2] = {f2(w0.x, w0.y), f2(w1.x, w1.y)};
-        uint32_t x[2][4];
+    // x of 16 tokens (block `tb` of the chunk) and this warp's 32 channels, transposed
+    auto fetch = [&](int st, int tb, uint32_t (&x)[2][4]) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int pp = q * 32 + half * 16 + pcol;
             ldsm_t(s0 + st * L.stage_bytes + (pp >> 6) * 8192 + (tb * 16 + row) * 128 + ((((pp & 63) >> 3) ^ (row & 7)) << 4), x[half]);
         }
+    };
+    // Xw of them, three exact pieces (the second negated)
+    auto weigh = [&](int i, int st, int tb, const uint32_t (&x)[2][4]) {
+        const uint32_t xw = tq + cXw + i * 96 + tb * 8;
+        const float* w = toks[st * HP + hw].w + tb * 16 + 2 * (lane & 3);
+        const float2 w0 = *reinterpret_cast<const float2*>(w), w1 = *reinterpret_cast<const float2*>(w + 8);
+        const F2 ww[2] = {f2(w0.x, w0.y), f2(w1.x, w1.y)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             uint32_t piece[3][4];
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     };
 
     if (warp < kInWarps) {
-        // ------------------------------------------------------------ operands of the chunk: Xw, C in 32 bits, W
+        // ------------------------------------------------------------ operands of the chunk: Xw, W, X^T
         regs_down<kInRegs>();
         int st = 0;
         uint32_t ph = 0;
@@ -261,33 +265,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         for (int c = 0; c < nch; ++c) {
             const ChunkTok* tok = toks + st * HP;
             loaded(c, st, ph);
-            if constexpr (!OUT) {
-                if (c >= 2) wait(kDs + (c & 1), ((c >> 1) - 1) & 1);  // Xw's buffer: the product that read it is done
-                tmem_fence_after_sync();
-                weigh(c & 1, st, part);
-                tmem_wait_st();
-                done(kXw + (c & 1));
-            } else {
-                if (c > 0) wait(kDs + HALVES - 1, (c - 1) & 1);
-                tmem_fence_after_sync();
-#pragma unroll 1
-                for (int tg = 0; tg < 2; ++tg) weigh(0, st, part * 2 + tg);
-                tmem_wait_st();
-                done(kXw);
-                if (c > 0) wait(kY, (c - 1) & 1);  // the buffers of C and W: the products that read them are done
-                // C: 8 values per lane and step, 8 rows side by side
-#pragma unroll 1
-                for (int i = warp * 32 + lane; i < 64 * (N / 8); i += kInWarps * 32) {
-                    const int rr = ((i >> 3) / (N / 8)) * 8 + (i & 7), cc = (i >> 3) % (N / 8);  // token, 8 values
-                    const uint4 v = *reinterpret_cast<const uint4*>(sm + st * L.stage_bytes + L.c_off + (cc >> 3) * 8192 + rr * 128 +
-                                                                    (((cc & 7) ^ (rr & 7)) << 4));
-                    unsigned char* to = sm + L.c32_off + (cc >> 2) * 8192 + rr * 128;
-                    const int at = (cc & 3) * 2;
-                    *reinterpret_cast<float4*>(to + ((at ^ (rr & 7)) << 4)) = make_float4(bf_lo(v.x), bf_hi(v.x), bf_lo(v.y), bf_hi(v.y));
-                    *reinterpret_cast<float4*>(to + (((at + 1) ^ (rr & 7)) << 4)) = make_float4(bf_lo(v.z), bf_hi(v.z), bf_lo(v.w), bf_hi(v.w));
-                }
-                fence_async_smem();
-                done(kC);
+            uint32_t x[2][2][4];
+#pragma unroll
+            for (int tg = 0; tg < 2; ++tg) fetch(st, part * 2 + tg, x[tg]);
+            if constexpr (OUT) {
+                auto read = [&]() {  // the chunk before is through with X^T, and with its buffer of W
+                    if (c > 0) wait(kY, (c - 1) & 1);
+                };
+                if (NBUF == 1) read();
                 wait(kG, c & 1);
                 tmem_fence_after_sync();
                 // Tokens j of block q reach tokens i of blocks cb = q..3; the quadrant's two warps take every second cb.
@@ -296,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     float gv[8];
                     tmem_ld_16x16(tq + cG + cb * 16, gv);
                     const int i0 = cb * 16 + 2 * (lane & 3);
-                    const uint32_t wbuf = L.w_off + j * 128 + 4 * (lane & 3);
+                    const uint32_t wbuf = L.w_off + (NBUF == 2 ? (c & 1) * HP * 16384 : 0) + j * 128 + 4 * (lane & 3);
                     const uint32_t at0 = wbuf + (((2 * cb) ^ (j & 7)) << 4), at1 = wbuf + (((2 * cb + 1) ^ (j & 7)) << 4);
                     auto put = [&](int h, int rb, int k, F2 w) {
                         const uint32_t at = (k ? at1 : at0) + h * 16384 + rb * 1024;
@@ -345,8 +330,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     }
                 }
                 fence_async_smem();
+                if (NBUF == 2) read();
+                tmem_fence_after_sync();
+#pragma unroll
+                for (int tg = 0; tg < 2; ++tg)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        tmem_st_16x8(tq + (static_cast<uint32_t>(half) << 20) + cX + part * 16 + tg * 8, x[tg][half][0], x[tg][half][1],
+                                     x[tg][half][2], x[tg][half][3]);
+                tmem_wait_st();
                 done(kW);
             }
+            // Xw's buffer: the product that read it is done
+            if (OUT && c > 0) wait(kDs + HALVES - 1, (c - 1) & 1);
+            if (!OUT && c >= 2) wait(kDs + (c & 1), ((c >> 1) - 1) & 1);
+            tmem_fence_after_sync();
+            const int xb = OUT ? 0 : c & 1;
+#pragma unroll
+            for (int tg = 0; tg < 2; ++tg) weigh(xb, st, part * 2 + tg, x[tg]);
+            tmem_wait_st();
+            done(kXw + xb);
             if (++st == L.stages) st = 0, ph ^= 1;
         }
     } else if (warp < kWarps) {
@@ -369,18 +372,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
 #pragma unroll
             for (int k = 0; k < NC / 2; ++k) S[k] = from ? f2(from[2 * k * P], from[(2 * k + 1) * P]) : f2(0.0f, 0.0f);
         }
-        auto put_state = [&]() {  // the state as an operand of Yb
+        auto put_state = [&]() {  // the state as an operand of Yb, two pieces (the second negated)
 #pragma unroll
             for (int k0 = 0; k0 < NC; k0 += NV) {
-                uint32_t v[NV];
+                uint32_t hi[NV / 2], lo[NV / 2];
 #pragma unroll
                 for (int k = 0; k < NV / 2; ++k) {
-                    float a, e;
-                    un(S[k0 / 2 + k], a, e);
-                    v[2 * k] = __float_as_uint(a);
-                    v[2 * k + 1] = __float_as_uint(e);
+                    F2 v = S[k0 / 2 + k];
+                    hi[k] = peel(v);
+                    lo[k] = pack_rn(v);
                 }
-                tmem_st_cols<NV>(tq + cS + part * NC + k0, v);
+                tmem_st_cols<NV / 2>(tq + cShi + (part * NC + k0) / 2, hi);
+                tmem_st_cols<NV / 2>(tq + cSlo + (part * NC + k0) / 2, lo);
             }
             tmem_wait_st();
             done(kS);
@@ -405,15 +408,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             }
         };
         if (OUT && nch > 0) put_state();
-        const uint32_t patch = L.patch_off + q * kPatch + part * (kPatch / 2);  // this warp's 32 tokens x 32 channels of y
         int st = 0;
         uint32_t ph = 0;
-        float before = 0.0f;  // the previous chunk's decay
         for (int c = 0; c < nch; ++c) {
             const ChunkTok& tok = toks[st * HP + hw];
             loaded(c, st, ph);
             const float decay = tok.dec;
             if constexpr (OUT) {
+                // this warp's 32 tokens x 32 channels of y
+                const uint32_t patch = L.patch_off + (NBUF == 2 ? (c & 1) * 4 * kPatch : 0) + q * kPatch + part * (kPatch / 2);
                 // The state takes dS before the outputs are there, but for the second half where dS comes in halves
                 // (one copy of both parts, for the instruction cache).
 #pragma unroll 1
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                         add_chunk(c, decay);
                         continue;
                     }
-                    if (c > 0) wait(kPatchFree, (c - 1) & 1);
+                    if (c >= NBUF) wait(kPatchFree + (NBUF == 2 ? c & 1 : 0), NBUF == 2 ? ((c >> 1) - 1) & 1 : (c - 1) & 1);
                     wait(kY, c & 1);
                     tmem_fence_after_sync();
                     const uint32_t ty = tq + part * 32;
@@ -441,6 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                             const uint32_t at = ty + (static_cast<uint32_t>((k4 + 1) & 1) << 20) + ((k4 + 1) >> 1) * 16;
                             tmem_ld_16x16(at + cYb, yb[now ^ 1]);
                             tmem_ld_16x16(at + cYa, ya[now ^ 1]);
+                        } else {
+                            done(kYfree);
                         }
                         uint32_t o[4];
 #pragma unroll
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     fence_async_smem();
                 }
                 if (c + 1 < nch) put_state();
-                done(kOut);  // (with the fence above: the patch is complete for the store)
+                done(kOut + (c & 1));  // (with the fence above: the patch is complete for the store)
                 if (ragged && c == nch - 1) {  // rows behind the sequence are not this call's to write
                     const int tok0 = r.first + c * kQ + part * 32, left = r.last - tok0;
                     const int64_t yrow = static_cast<int64_t>(p.H) * P;
@@ -468,21 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                 __syncwarp();
                 if (lane == 0) arrive(bar(kEmpty + st));
             } else {
-                if (c >= 2) wait(kDs + (c & 1), ((c >> 1) - 1) & 1);
-                tmem_fence_after_sync();
-                weigh(c & 1, st, 2 + part);
-                tmem_wait_st();
-                done(kXw + (c & 1));
-                if (c > 0) {
-                    add_chunk(c - 1, before);
-                    __syncwarp();
-                    if (lane == 0) arrive(bar(kEmpty + (st == 0 ? L.stages - 1 : st - 1)));
-                }
-                before = decay;
+                add_chunk(c, decay);
+                __syncwarp();
+                if (lane == 0) arrive(bar(kEmpty + st));
             }
             if (++st == L.stages) st = 0, ph ^= 1;
         }
-        if (!OUT && nch > 0) add_chunk(nch - 1, before);
         float* to = nullptr;
         if (mine) {
             if (!OUT) to = p.seg_state + (bh * p.split.slots() + seg) * np + own;
@@ -502,19 +498,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         auto load = [&](int c) {
             const int st = c % L.stages, t0 = r.first + c * kQ, nv = min(kQ, r.last - t0);
             const uint32_t base = s0 + st * L.stage_bytes;
-            if (lane == 0) {
-                arrive_tx(bar(kLanded + st), L.stage_bytes + heads * static_cast<uint32_t>(sizeof(ChunkTok)));
-                for (int h = 0; h < heads; ++h)
-                    bulk_load(s0 + L.tok_off + (st * HP + h) * static_cast<uint32_t>(sizeof(ChunkTok)), src + static_cast<int64_t>(h) * chunks + c,
-                              sizeof(ChunkTok), bar(kLanded + st));
-                tma_load_3d(base, &maps.x, g * cend + c0, t0, b, bar(kLanded + st));
-                tma_load_3d(base + 8192, &maps.x, g * cend + c0 + 64, t0, b, bar(kLanded + st));
-#pragma unroll
-                for (int k = 0; k < (N + 63) / 64; ++k) {
-                    tma_load_4d(base + L.b_off + k * 8192, &maps.b, k * 64, g, t0, b, bar(kLanded + st));
-                    if (OUT) tma_load_4d(base + L.c_off + k * 8192, &maps.c, k * 64, g, t0, b, bar(kLanded + st));
-                }
-            }
+            const uint32_t landed = bar(kLanded + st);
+            if (lane == 0) arrive_tx(landed, L.stage_bytes + heads * static_cast<uint32_t>(sizeof(ChunkTok)));
+            __syncwarp();
+            // one copy per lane: x, B and C in boxes of 64 columns, then the heads' decays
+            const int col = (lane & 1) * 64;
+            if (lane < 2) tma_load_3d(base + lane * 8192, &maps.x, g * cend + c0 + col, t0, b, landed);
+            else if (lane < 4 && col < N) tma_load_4d(base + L.b_off + (lane & 1) * 8192, &maps.b, col, g, t0, b, landed);
+            else if (OUT && lane >= 4 && lane < 6 && col < N) tma_load_4d(base + L.c_off + (lane & 1) * 8192, &maps.c, col, g, t0, b, landed);
+            else if (lane >= 6 && lane < 6 + heads)
+                bulk_load(s0 + L.tok_off + (st * HP + lane - 6) * static_cast<uint32_t>(sizeof(ChunkTok)),
+                          src + static_cast<int64_t>(lane - 6) * chunks + c, sizeof(ChunkTok), landed);
+            __syncwarp();
             issued = c + 1;
             if (nv < kQ) {
                 // rows behind the sequence may hold anything: zeros in their place
@@ -528,28 +523,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         };
 #pragma unroll 1
         for (int c = -L.stages; c < nch && !*abort_flag; ++c) {  // the first rounds only load
-            bool stored = false;
             if (OUT && c >= 0) {
-                wait(kOut, c & 1);
-                stored = !(ragged && c == nch - 1);
-                if (stored && lane == 0)
-                    for (int k = 0; k < 4; ++k)
-                        if (c0 + k * 32 < cend)
-                            tma_store_3d(&maps.y, g * cend + c0 + k * 32, r.first + c * kQ, b, s0 + L.patch_off + k * kPatch);
+                wait(kOut + (c & 1), (c >> 1) & 1);
+                if (!(ragged && c == nch - 1)) {
+                    if (lane < 4 && c0 + lane * 32 < cend) {
+                        tma_store_3d(&maps.y, g * cend + c0 + lane * 32, r.first + c * kQ, b,
+                                     s0 + L.patch_off + (NBUF == 2 ? (c & 1) * 4 * kPatch : 0) + lane * kPatch);
+                        store_read_done();
+                    }
+                    __syncwarp();
+                    if (lane == 0) arrive(bar(kPatchFree + (NBUF == 2 ? c & 1 : 0)));
+                }
             }
             if (c + L.stages < nch) {
                 if (c >= 0) wait(kEmpty + c % L.stages, (c / L.stages) & 1);
                 if (!*abort_flag) load(c + L.stages);
             }
-            if (stored) {
-                if (lane == 0) {
-                    store_read_done();
-                    arrive(bar(kPatchFree));
-                }
-                __syncwarp();
-            }
         }
-        if (OUT && lane == 0) store_done();
+        if (OUT && lane < 4) store_done();
         // no copy may land in this block's memory after it has gone (bounded, also after an abort)
         if (*abort_flag && lane == 0) {
             const uint64_t t_end = now_ns() + 2000000000ull;
@@ -561,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         // ------------------------------------------------------------ MMA issue: G and dS (whole warp, one lane issues)
         regs_down<kMiscRegs>();
         constexpr int ND = HALVES == 2 ? 64 : N;  // columns of one dS product
-        constexpr uint32_t wG = mma_word(64, 64, false, false), wDs = mma_word(128, ND, false, true);
+        constexpr uint32_t wG = mma_word(64, 64, false, false), wDs = mma_word(128, ND, false, true), wDsNeg = mma_word(128, ND, false, true, true);
         auto issue_g = [&](int st) {
             const Desc along = desc_of(s0 + st * L.stage_bytes, 16);  // B and C as [token, n]: contraction along the rows
             tmem_fence_after_sync();
@@ -582,18 +573,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                 for (int s = 2; s >= 0; --s)  // the small pieces first
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma_ts(tm + cDs + (OUT ? 0 : i * 128), tm + cXw + xb * 96 + s * 32 + k * 8, down + k * 2048, wDs, s < 2 || k > 0);
+                        mma_ts(tm + cDs + (OUT ? 0 : i * 128), tm + cXw + xb * 96 + s * 32 + k * 8, down + k * 2048, s == 1 ? wDsNeg : wDs,
+                               s < 2 || k > 0);
                 mma_commit(bar(kDs + i));
             }
             __syncwarp();
         };
         int st = 0;
         uint32_t ph = 0;
+        if (OUT && nch > 0) {
+            loaded(0, 0, 0);
+            issue_g(0);
+        }
         for (int c = 0; c < nch && !*abort_flag; ++c) {
-            loaded(c, st, ph);
+            const int st1 = st + 1 == L.stages ? 0 : st + 1;
+            const uint32_t ph1 = st1 == 0 ? ph ^ 1 : ph;
             if constexpr (OUT) {
-                if (c > 0) wait(kW, (c - 1) & 1);  // G's columns have been read
-                issue_g(st);
+                wait(kW, c & 1);  // G's columns have been read
+                if (c + 1 < nch) {
+                    loaded(c + 1, st1, ph1);
+                    issue_g(st1);
+                }
                 wait(kXw, c & 1);
                 if (c > 0) wait(kDsFree + HALVES - 1, (c - 1) & 1);
 #pragma unroll 1
@@ -602,33 +602,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     issue_ds(half, 0, half, st);
                 }
             } else {
+                loaded(c, st, ph);
                 wait(kXw + (c & 1), (c >> 1) & 1);
                 if (c >= 2) wait(kDsFree + (c & 1), ((c >> 1) - 1) & 1);
                 issue_ds(c & 1, c & 1, 0, st);
             }
-            if (++st == L.stages) st = 0, ph ^= 1;
+            st = st1, ph = ph1;
         }
         drain(kDrain);
     } else if (warp == kMmaWarp + 1) {
         // ------------------------------------------------------------ MMA issue: Yb and Ya
         regs_down<kMiscRegs>();
         if constexpr (OUT) {
-            constexpr uint32_t wYb = mma_word_tf32(128, 64), wYa = mma_word(128, 64, true, true);
-            const Desc along = desc_of(s0 + L.c32_off, 16);  // C as [i, n]: contraction along the rows
-            const Desc wd = desc_of(s0 + L.w_off, 8192);
             int st = 0;
             for (int c = 0; c < nch && !*abort_flag; ++c) {
-                const Desc down = desc_of(s0 + st * L.stage_bytes, 8192);  // x as [j, p]: contraction down the rows
-                wait(kC, c & 1);  // C is there, and with it x
-                wait(kS, c & 1);  // the state is there, and the columns of Ya and Yb have been read
-                tmem_fence_after_sync();
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < N / 8; ++k)
-                        mma_ts_tf32(tm + cYb, tm + cS + k * 8, along + ((k >> 2) * 8192 + (k & 3) * 32), wYb, k > 0);
-                }
-                __syncwarp();
-                wait(kW, c & 1);
+                const Desc along = desc_of(s0 + st * L.stage_bytes + L.c_off, 16);  // C as [i, n]: contraction along the rows
+                const Desc wd = desc_of(s0 + L.w_off + (NBUF == 2 ? (c & 1) * HP * 16384 : 0), 8192);
+                wait(kW, c & 1);                       // W and X^T are there
+                if (c > 0) wait(kYfree, (c - 1) & 1);  // the columns of Ya and Yb have been read
                 tmem_fence_after_sync();
                 if (elect_one()) {
 #pragma unroll
@@ -637,14 +628,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                         for (int s = 0; s < 2; ++s)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const Desc da = down + k * 2048, db = wd + (h * 16384 + (s ? 0 : 8192) + k * 2048);
+                                const Desc db = wd + (h * 16384 + (s ? 0 : 8192) + k * 2048);
+                                constexpr uint32_t w0 = mma_word(128, 64, false, true, false, true), w1 = mma_word(128, 64, false, true);
                                 if constexpr (HP == 1) {
-                                    mma_ss(tm + cYa, da, db, wYa, s + k > 0);
+                                    mma_ts(tm + cYa, tm + cX + k * 8, db, s ? w1 : w0, s + k > 0);
                                 } else {
                                     auto off = [&](int qq) { return (HP == 4 ? qq : qq >> 1) == h ? 0u : 0xffffffffu; };
-                                    mma_ss_masked(tm + cYa, da, db, wYa, off(0), off(1), off(2), off(3), s + k > 0);
+                                    mma_ts_masked(tm + cYa, tm + cX + k * 8, db, s ? w1 : w0, off(0), off(1), off(2), off(3), s + k > 0);
                                 }
                             }
+                }
+                __syncwarp();
+                wait(kS, c & 1);
+                tmem_fence_after_sync();
+                if (elect_one()) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int k = 0; k < N / 16; ++k)
+                            mma_ts(tm + cYb, tm + (s ? cShi : cSlo) + k * 8, along + ((k >> 2) * 8192 + (k & 3) * 32),
+                                   s ? mma_word(128, 64, false, false) : mma_word(128, 64, false, false, true), s + k > 0);
                     mma_commit(bar(kY));
                 }
                 __syncwarp();
