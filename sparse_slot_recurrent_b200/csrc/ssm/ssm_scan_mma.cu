@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
             int count = 1;  // a commit, a copy or one warp
-            if ((i >= kEmpty && i < kEmpty + 4) || i == kS || i == kYfree || i == kOut || i == kOut + 1) count = kOutWarps;
+            if (i == kS) count = kOutWarps;
+            if ((i >= kEmpty && i < kEmpty + 4) || i == kYfree || i == kOut || i == kOut + 1) count = OUT ? kWarps : kOutWarps;
             if (i == kW || i == kXw || i == kXw + 1) count = kInWarps;
             if (i == kDsFree || i == kDsFree + 1) count = kOutWarps / HALVES;
             mbar_init(bar_mem + i, count);
@@ -246,6 +247,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                 tmem_st_16x8(xw + (static_cast<uint32_t>(half) << 20) + s * 32, piece[s][0], piece[s][1], piece[s][2], piece[s][3]);
         }
     };
+    // y of chunk c, 16 tokens (block tb) x this warp's 32 channels, through registers into the patch that the load warp
+    // stores.  Chunk c is known to be in its stage: its products waited for that.
+    auto outputs = [&](int c, int st, int tb) {
+        const uint32_t patch = L.patch_off + (NBUF == 2 ? (c & 1) * 4 * kPatch : 0) + q * kPatch + tb * 1024;
+        const uint32_t ty = tq + tb * 16;
+        float yb[2][8], ya[2][8];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            tmem_ld_16x16(ty + (static_cast<uint32_t>(half) << 20) + cYb, yb[half]);
+            tmem_ld_16x16(ty + (static_cast<uint32_t>(half) << 20) + cYa, ya[half]);
+        }
+        const float* e = toks[st * HP + hw].ein + tb * 16 + 2 * (lane & 3);
+        const float2 e0 = *reinterpret_cast<const float2*>(e), e1 = *reinterpret_cast<const float2*>(e + 8);
+        tmem_wait_ld();
+        done(kYfree);
+        if (c >= NBUF) wait(kPatchFree + (NBUF == 2 ? c & 1 : 0), NBUF == 2 ? ((c >> 1) - 1) & 1 : (c - 1) & 1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            settle(yb[half]);
+            settle(ya[half]);
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // 8 tokens k/2, 8 channels k%2
+                const int at = 4 * (k >> 1) + 2 * (k & 1);
+                const float2 ee = k < 2 ? e0 : e1;
+                o[k] = pack_rn(fma2(f2(ee.x, ee.y), f2(yb[half][at], yb[half][at + 1]), f2(ya[half][at], ya[half][at + 1])));
+            }
+            stsm_t(s0 + patch + row * 64 + (((half * 2 + (pcol >> 3)) ^ ((row >> 1) & 3)) << 4), o[0], o[1], o[2], o[3]);
+        }
+        if (ragged && c == nch - 1) {  // rows behind the sequence are not this call's to write
+            __syncwarp();
+            const int tok0 = r.first + c * kQ + tb * 16, left = r.last - tok0;
+            const int64_t yrow = static_cast<int64_t>(p.H) * P;
+            __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.T + tok0) * yrow + g * cend + c0 + q * 32 + (lane & 3) * 8;
+#pragma unroll 1
+            for (int t = lane >> 2; t < min(left, 16) && c0 + q * 32 < cend; t += 8)
+                *reinterpret_cast<uint4*>(yp + t * yrow) = *reinterpret_cast<const uint4*>(sm + patch + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
+        }
+        fence_async_smem();
+        done(kOut + (c & 1));
+    };
     auto drain = [&](int i) {  // after an abort: tensor memory is given back only when nothing writes to it
         if (*abort_flag && lane == 0) {
             const uint64_t t_end = now_ns() + 2000000000ull;
@@ -269,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
 #pragma unroll
             for (int tg = 0; tg < 2; ++tg) fetch(st, part * 2 + tg, x[tg]);
             if constexpr (OUT) {
-                auto read = [&]() {  // the chunk before is through with X^T, and with its buffer of W
+                auto read = [&]() {  // the chunk before is through with X^T, and with its buffer of W; its outputs are there
                     if (c > 0) wait(kY, (c - 1) & 1);
                 };
                 if (NBUF == 1) read();
@@ -340,6 +382,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                                      x[tg][half][2], x[tg][half][3]);
                 tmem_wait_st();
                 done(kW);
+                if (c > 0) {  // every second block of the outputs before
+                    const int before = st == 0 ? L.stages - 1 : st - 1;
+                    outputs(c - 1, before, part * 2 + 1);
+                    if (lane == 0) arrive(bar(kEmpty + before));
+                }
             }
             // Xw's buffer: the product that read it is done
             if (OUT && c > 0) wait(kDs + HALVES - 1, (c - 1) & 1);
@@ -351,6 +398,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             tmem_wait_st();
             done(kXw + xb);
             if (++st == L.stages) st = 0, ph ^= 1;
+        }
+        if (OUT && nch > 0) {
+            wait(kY, (nch - 1) & 1);
+            tmem_fence_after_sync();
+            outputs(nch - 1, st == 0 ? L.stages - 1 : st - 1, part * 2 + 1);
         }
     } else if (warp < kWarps) {
         // ------------------------------------------------------------ state and outputs
@@ -388,10 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             tmem_wait_st();
             done(kS);
         };
-        auto add_chunk = [&](int c, float decay) {  // S' = dec S + dS
+        auto add_chunk = [&](int c, int st) {  // S' = dec S + dS
             const int i = OUT ? (HALVES == 2 ? part : 0) : c & 1;
             wait(kDs + i, OUT ? c & 1 : (c >> 1) & 1);
             tmem_fence_after_sync();
+            const float decay = toks[st * HP + hw].dec;
             const F2 dec = f2(decay, decay);
             const uint32_t td = tq + cDs + (OUT ? 0 : i * 128) + (HALVES == 2 ? 0 : part * NC);
             float d[2][NV];
@@ -411,72 +464,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         int st = 0;
         uint32_t ph = 0;
         for (int c = 0; c < nch; ++c) {
-            const ChunkTok& tok = toks[st * HP + hw];
-            loaded(c, st, ph);
-            const float decay = tok.dec;
             if constexpr (OUT) {
-                // this warp's 32 tokens x 32 channels of y
-                const uint32_t patch = L.patch_off + (NBUF == 2 ? (c & 1) * 4 * kPatch : 0) + q * kPatch + part * (kPatch / 2);
                 // The state takes dS before the outputs are there, but for the second half where dS comes in halves
                 // (one copy of both parts, for the instruction cache).
 #pragma unroll 1
                 for (int step = 0; step < 2; ++step) {
                     if (step == (HALVES == 2 ? part : 0)) {
-                        add_chunk(c, decay);
-                        continue;
+                        add_chunk(c, st);
+                    } else {
+                        wait(kY, c & 1);
+                        tmem_fence_after_sync();
+                        outputs(c, st, part * 2);
                     }
-                    if (c >= NBUF) wait(kPatchFree + (NBUF == 2 ? c & 1 : 0), NBUF == 2 ? ((c >> 1) - 1) & 1 : (c - 1) & 1);
-                    wait(kY, c & 1);
-                    tmem_fence_after_sync();
-                    const uint32_t ty = tq + part * 32;
-                    float yb[2][8], ya[2][8];
-                    tmem_ld_16x16(ty + cYb, yb[0]);
-                    tmem_ld_16x16(ty + cYa, ya[0]);
-#pragma unroll
-                    for (int k4 = 0; k4 < 4; ++k4) {  // 16 tokens k4/2, 16 channels k4%2; the next loads run meanwhile
-                        const int now = k4 & 1, tg = k4 >> 1;
-                        const float* e = tok.ein + part * 32 + tg * 16 + 2 * (lane & 3);
-                        const float2 e0 = *reinterpret_cast<const float2*>(e), e1 = *reinterpret_cast<const float2*>(e + 8);
-                        tmem_wait_ld();
-                        settle(yb[now]);
-                        settle(ya[now]);
-                        if (k4 < 3) {
-                            const uint32_t at = ty + (static_cast<uint32_t>((k4 + 1) & 1) << 20) + ((k4 + 1) >> 1) * 16;
-                            tmem_ld_16x16(at + cYb, yb[now ^ 1]);
-                            tmem_ld_16x16(at + cYa, ya[now ^ 1]);
-                        } else {
-                            done(kYfree);
-                        }
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {  // 8 tokens k/2, 8 channels k%2
-                            const int at = 4 * (k >> 1) + 2 * (k & 1);
-                            const float2 ee = k < 2 ? e0 : e1;
-                            o[k] = pack_rn(fma2(f2(ee.x, ee.y), f2(yb[now][at], yb[now][at + 1]), f2(ya[now][at], ya[now][at + 1])));
-                        }
-                        stsm_t(s0 + patch + (tg * 16 + row) * 64 + ((((k4 & 1) * 2 + (pcol >> 3)) ^ ((row >> 1) & 3)) << 4), o[0], o[1], o[2], o[3]);
-                    }
-                    fence_async_smem();
                 }
                 if (c + 1 < nch) put_state();
-                done(kOut + (c & 1));  // (with the fence above: the patch is complete for the store)
-                if (ragged && c == nch - 1) {  // rows behind the sequence are not this call's to write
-                    const int tok0 = r.first + c * kQ + part * 32, left = r.last - tok0;
-                    const int64_t yrow = static_cast<int64_t>(p.H) * P;
-                    __nv_bfloat16* yp = reinterpret_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.T + tok0) * yrow + g * cend + c0 +
-                                        q * 32 + (lane & 3) * 8;
-#pragma unroll 1
-                    for (int t = lane >> 2; t < min(left, 32) && c0 + q * 32 < cend; t += 8)
-                        *reinterpret_cast<uint4*>(yp + t * yrow) =
-                            *reinterpret_cast<const uint4*>(sm + patch + t * 64 + (((lane & 3) ^ ((t >> 1) & 3)) << 4));
-                }
-                __syncwarp();
-                if (lane == 0) arrive(bar(kEmpty + st));
             } else {
-                add_chunk(c, decay);
-                __syncwarp();
-                if (lane == 0) arrive(bar(kEmpty + st));
+                loaded(c, st, ph);
+                add_chunk(c, st);
             }
+            __syncwarp();
+            if (lane == 0) arrive(bar(kEmpty + st));
             if (++st == L.stages) st = 0, ph ^= 1;
         }
         float* to = nullptr;
