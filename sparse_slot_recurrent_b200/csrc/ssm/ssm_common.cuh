@@ -6,6 +6,27 @@
 
 namespace ramnet {
 
+// The scan's launches follow one another as programmatic dependents: a launch may start, and set itself up, while the
+// one before still runs; after_before() waits for all of that one's memory, let_next() allows the next to start.
+__device__ __forceinline__ void after_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class... Args>
+cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, Args... args)
+{
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Step size of one token and head: softplus(dt + bias) (or dt + bias), clamped.
 __device__ __forceinline__ float step_size(float dt, float bias, int softplus, float lo, float hi)
 {

@@ -116,6 +116,8 @@ __global__ void __launch_bounds__(128) k_ssm_scan(SsmParams p)
 __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
 {
     __shared__ float decay[256];
+    let_next();
+    after_before();
     const int np4 = p.N * p.P / 4;
     const int e = blockIdx.x * 256 + threadIdx.x;
     const int64_t bh = blockIdx.y;
@@ -179,9 +181,10 @@ cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t s)
         if (p.toks) q.toks = p.toks + at * ((p.T + kChunk - 1) / kChunk);
         q.chain_first = at;
         const int64_t rows = bh - at < 65535 ? bh - at : 65535;
-        k_ssm_chain<<<dim3(static_cast<unsigned>((np / 4 + 255) / 256), static_cast<unsigned>(rows)), 256, 0, s>>>(q);
+        const cudaError_t e = launch_dependent(k_ssm_chain, dim3(static_cast<unsigned>((np / 4 + 255) / 256), static_cast<unsigned>(rows)), 256, 0, s, q);
+        if (e != cudaSuccess) return e;
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 // As many segments as fill 148 SMs with one block of 128 channels each, none shorter than 256

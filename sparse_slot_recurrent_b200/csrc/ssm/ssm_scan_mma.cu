@@ -34,8 +34,8 @@
 namespace ramnet {
 namespace {
 
-// Registers per thread by role: 20 warps launch with 96 each, and 2 x 80 + 2 x 128 + 64 = 5 x 96.
-constexpr int kInRegs = 80, kOutRegs = 128, kMiscRegs = 64;
+// Registers per thread by role: 20 warps launch with 96 each, and 2 x 88 + 2 x 128 + 48 = 5 x 96.
+constexpr int kInRegs = 88, kOutRegs = 128, kMiscRegs = 48;
 constexpr int kQ = kChunk;       // tokens per chunk
 constexpr int kInWarps = 8, kOutWarps = 8, kWarps = kInWarps + kOutWarps;
 constexpr int kLoadWarp = 16, kMmaWarp = 18;
@@ -84,6 +84,7 @@ __device__ __forceinline__ float ex2(float v)
 // Step sizes and decays of every chunk: one warp per (sequence, head, chunk), two tokens per lane, sums in 64 bits.
 __global__ void __launch_bounds__(256) k_ssm_decay(const SsmParams p, int chunks, int64_t work)
 {
+    let_next();
     const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     if (id >= work) return;
     const int lane = threadIdx.x & 31;
@@ -199,9 +200,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         for (uint32_t i = threadIdx.x; i < NBUF * HP * 1024u; i += kThreads) w[i] = make_uint4(0, 0, 0, 0);
         fence_async_smem();
     }
+    if (!OUT) let_next();
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
+    after_before();
     constexpr uint32_t tm = 0;  // where an allocation of all 512 columns starts
 
     const int q = warp & 3, part = (warp >> 2) & 1;             // tensor-memory quadrant; half of the tokens or state columns
@@ -723,8 +726,7 @@ cudaError_t go(const SsmParams& p, const MmaMaps& m, int tiles, int segs, cudaSt
     auto kern = k_ssm_mma<N, P, OUT>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L.total));
     if (e != cudaSuccess) return e;
-    kern<<<dim3(static_cast<unsigned>(p.B) * p.G * tiles, segs), kThreads, L.total, s>>>(m, p, tiles);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(static_cast<unsigned>(p.B) * p.G * tiles, segs), kThreads, L.total, s, m, p, tiles);
 }
 
 template <int N, int P>
