@@ -8,7 +8,6 @@ to load, every call raises -- there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -369,53 +368,68 @@ def _strides_of(b: int, t: int, h: int):
     return ctypes.pointer(_Strides(b, t, h))
 
 
-def _arg(t, name, shape, dtype, like, dense=True):
-    """Pointer of an operand after its checks (None stays None)."""
-    if t is None:
-        return None
+def _refuse(t, name, shape, dtype, dev, dense):
+    """Raises for the first thing that is wrong with an operand."""
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, {tuple(shape)} expected")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, {dtype} expected")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, {like.device} expected")
-    if dense and not t.is_contiguous():
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, cuda:{dev} expected")
+    if dense:
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
-def _in(t, name):
-    """Input dtype code; the operand must be on a GPU with its last dimension contiguous."""
-    code = _DTYPES.get(t.dtype)
+def _dense_ptr(t, name, shape, dtype, dev):
+    """Pointer of a contiguous operand after its checks (None stays None)."""
+    if t is None:
+        return None
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, shape, dtype, dev, True)
+
+
+def _rows_ptr(t, name, shape, dtype, dev):
+    """Pointer of an operand that only needs its last dimension contiguous."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and (t.stride(-1) == 1 or t.shape[-1] == 1):
+        return t.data_ptr()
+    _refuse(t, name, shape, dtype, dev, False)
+
+
+def _input(x, name):
+    """Dtype code and device index of the operand that the others go by."""
+    code = _DTYPES.get(x.dtype)
     if code is None:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if not t.is_cuda:
+        raise TypeError(f"{name}: unsupported dtype {x.dtype}")
+    if not x.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    return code
+    return code, x.get_device()
 
 
-def _last_contiguous(*pairs):
-    for t, name in pairs:
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise ValueError(f"the last dimension of {name} must be contiguous")
-
-
-def _on(t):
-    """Makes t's device current for a launch, where it is not."""
-    return contextlib.nullcontext() if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-
-def _out(y, name, shape, out_dtype, x):
+def _output(y, name, shape, out_dtype, x, dev):
     """The output tensor (allocated if not given) and its dtype code."""
     if y is None:
         y = torch.empty(shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
-    elif out_dtype is not None and y.dtype != out_dtype:
+    elif out_dtype is not None and y.dtype is not out_dtype:
         raise TypeError(f"{name} is {y.dtype}, out_dtype is {out_dtype}")
+    else:
+        _dense_ptr(y, name, shape, y.dtype, dev)
     code = _DTYPES.get(y.dtype)
     if code is None:
         raise TypeError(f"{name}: unsupported dtype {y.dtype}")
-    _arg(y, name, torch.Size(shape), y.dtype, x)
     return y, code
+
+
+def _launch(dev, stream, call, *args):
+    """Calls the library with dev current and the stream (dev's current one if None) as the last argument.  The two
+    lookups are the ones behind torch.cuda.current_device and current_stream, whose wrappers cost more than a launch."""
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return _launch(dev, stream, call, *args)
+    status = call(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status != RAMNET_OK:
+        raise RamnetError(status, last_error())
 
 
 def ssm_workspace_bytes(cfg: SsmConfig, B: int, T: int) -> int:
@@ -424,15 +438,15 @@ def ssm_workspace_bytes(cfg: SsmConfig, B: int, T: int) -> int:
 
 def _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias):
     """Checked operands shared by the two forms: lead is [B] or [B, T]."""
-    lead, H, G, N = x.shape[:-2], cfg.H, cfg.G, cfg.N
-    code = _in(x, "x")
-    f32 = torch.float32
-    ptrs = (_arg(x, "x", (*lead, H, cfg.P), x.dtype, x, False), _arg(dt, "dt", (*lead, H), x.dtype, x, False),
-            _arg(A, "A", (H,), f32, x), _arg(Bm, "Bm", (*lead, G, N), x.dtype, x, False),
-            _arg(Cm, "Cm", (*lead, G, N), x.dtype, x, False), _arg(D, "D", (H,), f32, x),
-            _arg(dt_bias, "dt_bias", (H,), f32, x))
-    _last_contiguous((x, "x"), (Bm, "Bm"), (Cm, "Cm"))
-    return code, ptrs
+    code, dev = _input(x, "x")
+    lead, H, t, f32 = x.shape[:-2], cfg.H, x.dtype, torch.float32
+    bc = (*lead, cfg.G, cfg.N)
+    px = _rows_ptr(x, "x", (*lead, H, cfg.P), t, dev)
+    if dt.shape != (*lead, H) or dt.dtype is not t or dt.get_device() != dev:
+        _refuse(dt, "dt", (*lead, H), t, dev, False)
+    return code, dev, (px, dt.data_ptr(), _dense_ptr(A, "A", (H,), f32, dev), _rows_ptr(Bm, "Bm", bc, t, dev),
+                       _rows_ptr(Cm, "Cm", bc, t, dev), _dense_ptr(D, "D", (H,), f32, dev),
+                       _dense_ptr(dt_bias, "dt_bias", (H,), f32, dev))
 
 
 def ssm_forward(cfg: SsmConfig, x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=None, S_in=None, out_dtype=None, y=None,
@@ -441,43 +455,35 @@ def ssm_forward(cfg: SsmConfig, x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=
     with the last dimension of x, Bm and Cm contiguous), A, D, dt_bias [H] fp32, lengths [B] int32.
     Returns (y [B,T,H,P] in out_dtype (x's if None), S_out [B,H,N,P] fp32).  Rows of a y that is passed in
     behind a sequence's last token keep their values; S_out may be S_in."""
+    code, dev, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
     B, T = x.shape[:2]
-    code, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
-    state = torch.Size((B, cfg.H, cfg.N, cfg.P))
-    plen = _arg(lengths, "lengths", (B,), torch.int32, x)
-    pin = _arg(S_in, "S_in", state, torch.float32, x)
-    y, ycode = _out(y, "y", x.shape, out_dtype, x)
+    state = (B, cfg.H, cfg.N, cfg.P)
+    plen = _dense_ptr(lengths, "lengths", (B,), torch.int32, dev)
+    pin = _dense_ptr(S_in, "S_in", state, torch.float32, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
     if S_out is None:
         S_out = torch.empty(state, dtype=torch.float32, device=x.device)
-    pout = _arg(S_out, "S_out", state, torch.float32, x)
+    pout = _dense_ptr(S_out, "S_out", state, torch.float32, dev)
     if workspace is None:
-        need = ssm_workspace_bytes(cfg, B, T)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    nbytes = 0
-    if workspace is not None:
-        if not workspace.is_contiguous() or workspace.device != x.device:
-            raise ValueError("workspace must be contiguous and on the device of x")
-        nbytes = workspace.numel() * workspace.element_size()
-    with _on(x):
-        _check(load().ramnet_ssm_forward(cfg._ref, B, T, code, px, _strides_of(*x.stride()[:3]), pdt,
-                                         _strides_of(*dt.stride()), pA, pB, _strides_of(*Bm.stride()[:3]), pC,
-                                         _strides_of(*Cm.stride()[:3]), pD, pbias, plen, pin, y.data_ptr(), ycode, pout,
-                                         _ptr(workspace), nbytes, _stream(stream)))
+        workspace = torch.empty(ssm_workspace_bytes(cfg, B, T), dtype=torch.uint8, device=x.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be contiguous and on the device of x")
+    _launch(dev, stream, load().ramnet_ssm_forward, cfg._ref, B, T, code, px, _strides_of(*x.stride()[:3]), pdt,
+            _strides_of(*dt.stride()), pA, pB, _strides_of(*Bm.stride()[:3]), pC, _strides_of(*Cm.stride()[:3]), pD, pbias,
+            plen, pin, y.data_ptr(), ycode, pout, workspace.data_ptr(), workspace.nbytes)
     return y, S_out
 
 
 def ssm_step(cfg: SsmConfig, x, dt, A, Bm, Cm, S, D=None, dt_bias=None, out_dtype=None, y=None, stream=None):
     """Selective scan for one token per sequence: x [B,H,P], dt [B,H], Bm and Cm [B,G,N]; S [B,H,N,P] fp32 is
     updated in place.  Returns y [B,H,P]."""
+    code, dev, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
     B = x.shape[0]
-    code, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
-    pS = _arg(S, "S", (B, cfg.H, cfg.N, cfg.P), torch.float32, x)
-    y, ycode = _out(y, "y", x.shape, out_dtype, x)
+    pS = _dense_ptr(S, "S", (B, cfg.H, cfg.N, cfg.P), torch.float32, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
     (xb, xh, _), (db, dh), (bb, bg, _), (cb, cg, _) = x.stride(), dt.stride(), Bm.stride(), Cm.stride()
-    with _on(x):
-        _check(load().ramnet_ssm_step(cfg._ref, B, code, px, _strides_of(xb, 0, xh), pdt, _strides_of(db, 0, dh), pA, pB,
-                                      _strides_of(bb, 0, bg), pC, _strides_of(cb, 0, cg), pD, pbias, pS, y.data_ptr(),
-                                      ycode, _stream(stream)))
+    _launch(dev, stream, load().ramnet_ssm_step, cfg._ref, B, code, px, _strides_of(xb, 0, xh), pdt, _strides_of(db, 0, dh), pA,
+            pB, _strides_of(bb, 0, bg), pC, _strides_of(cb, 0, cg), pD, pbias, pS, y.data_ptr(), ycode)
     return y
 
 
@@ -486,51 +492,41 @@ def conv_forward(x, w, bias=None, silu=True, lengths=None, state_in=None, out_dt
     """Short causal convolution over a prompt: x [B,T,C] (bf16 or fp32, channels contiguous), w [C,W] and
     bias [C] fp32, state_in [B,W-1,C] in x's dtype (the inputs before the first token; zeros if None).
     Returns (y [B,T,C], state_out [B,W-1,C]); state_out may be state_in."""
-    B, T, C = x.shape
-    W = w.shape[1]
-    code = _in(x, "x")
-    _last_contiguous((x, "x"))
-    pw, pb = _arg(w, "w", (C, W), torch.float32, x), _arg(bias, "bias", (C,), torch.float32, x)
-    plen = _arg(lengths, "lengths", (B,), torch.int32, x)
-    pin = _arg(state_in, "state_in", (B, W - 1, C), x.dtype, x)
-    y, ycode = _out(y, "y", x.shape, out_dtype, x)
+    code, dev = _input(x, "x")
+    (B, T, C), W, t, f32 = x.shape, w.shape[1], x.dtype, torch.float32
+    px, pw, pb = _rows_ptr(x, "x", x.shape, t, dev), _dense_ptr(w, "w", (C, W), f32, dev), _dense_ptr(bias, "bias", (C,), f32, dev)
+    plen = _dense_ptr(lengths, "lengths", (B,), torch.int32, dev)
+    pin = _dense_ptr(state_in, "state_in", (B, W - 1, C), t, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
     if state_out is None:
-        state_out = torch.empty((B, W - 1, C), dtype=x.dtype, device=x.device)
-    pout = _arg(state_out, "state_out", (B, W - 1, C), x.dtype, x)
-    with _on(x):
-        _check(load().ramnet_conv_forward(B, T, C, W, code, x.data_ptr(), x.stride(0), x.stride(1), pw, pb, bool(silu), plen,
-                                          pin, y.data_ptr(), ycode, pout, _stream(stream)))
+        state_out = torch.empty((B, W - 1, C), dtype=t, device=x.device)
+    pout = _dense_ptr(state_out, "state_out", (B, W - 1, C), t, dev)
+    _launch(dev, stream, load().ramnet_conv_forward, B, T, C, W, code, px, x.stride(0), x.stride(1), pw, pb, bool(silu), plen, pin,
+            y.data_ptr(), ycode, pout)
     return y, state_out
 
 
 def conv_step(x, w, state, bias=None, silu=True, out_dtype=None, y=None, stream=None):
     """The convolution for one token per sequence: x [B,C]; state [B,W-1,C] in x's dtype takes the token in
     and drops its oldest.  Returns y [B,C]."""
-    B, C = x.shape
-    W = w.shape[1]
-    code = _in(x, "x")
-    _last_contiguous((x, "x"))
-    pw, pb = _arg(w, "w", (C, W), torch.float32, x), _arg(bias, "bias", (C,), torch.float32, x)
-    ps = _arg(state, "state", (B, W - 1, C), x.dtype, x)
-    y, ycode = _out(y, "y", x.shape, out_dtype, x)
-    with _on(x):
-        _check(load().ramnet_conv_step(B, C, W, code, x.data_ptr(), x.stride(0), pw, pb, bool(silu), ps, y.data_ptr(), ycode,
-                                       _stream(stream)))
+    code, dev = _input(x, "x")
+    (B, C), W, t, f32 = x.shape, w.shape[1], x.dtype, torch.float32
+    px, pw, pb = _rows_ptr(x, "x", x.shape, t, dev), _dense_ptr(w, "w", (C, W), f32, dev), _dense_ptr(bias, "bias", (C,), f32, dev)
+    ps = _dense_ptr(state, "state", (B, W - 1, C), t, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
+    _launch(dev, stream, load().ramnet_conv_step, B, C, W, code, px, x.stride(0), pw, pb, bool(silu), ps, y.data_ptr(), ycode)
     return y
 
 
 def norm_gate(x, z=None, w=None, groups=1, eps=1e-6, gate_first=True, out_dtype=None, y=None, stream=None):
     """RMSNorm of the rows of x [R,D] over ``groups`` groups of channels, times w [D] fp32, gated by silu(z)
     (z [R,D], None: no gate) before the norm or behind it.  Returns y [R,D]."""
+    code, dev = _input(x, "x")
     R, D = x.shape
-    code = _in(x, "x")
-    _last_contiguous((x, "x"))
-    pz = _arg(z, "z", (R, D), x.dtype, x, False)
-    if z is not None:
-        _last_contiguous((z, "z"))
-    pw = _arg(w, "w", (D,), torch.float32, x)
-    y, ycode = _out(y, "y", x.shape, out_dtype, x)
-    with _on(x):
-        _check(load().ramnet_norm_gate(R, D, groups, code, x.data_ptr(), x.stride(0), pz, 0 if z is None else z.stride(0), pw,
-                                       eps, bool(gate_first), y.data_ptr(), ycode, _stream(stream)))
+    px = _rows_ptr(x, "x", x.shape, x.dtype, dev)
+    pz, zs = (None, 0) if z is None else (_rows_ptr(z, "z", x.shape, x.dtype, dev), z.stride(0))
+    pw = _dense_ptr(w, "w", (D,), torch.float32, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
+    _launch(dev, stream, load().ramnet_norm_gate, R, D, groups, code, px, x.stride(0), pz, zs, pw, eps, bool(gate_first),
+            y.data_ptr(), ycode)
     return y
