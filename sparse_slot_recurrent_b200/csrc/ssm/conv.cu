@@ -5,74 +5,24 @@
 //
 // Bound: HBM, one read of x and one write of y (2 W flops per element).  A thread owns V
 // neighbouring channels (16 bytes where addresses allow) over a run of tokens and slides a
-// window of W-1 inputs in registers, so each input is read once but for W-1 rows per run.
-#include "../common.cuh"
-#include "ssm.h"
+// window of W-1 inputs in registers, so each input is read once but for W-1 rows per run (which
+// the run before has just brought into L2).  Rows come through a ring in shared memory that
+// only its own thread fills and reads, up to twelve in flight (for 4 x 16384 x 2304 bf16 channels: 273 us with one
+// load at a time behind the store before it, 209 us with four in registers).  Products and sums run on pairs of channels.
+#include "rows.cuh"
 
 namespace ramnet {
 namespace {
 
 constexpr int kConvRun = 32;  // tokens per thread
 
-template <bool BF>
-using InT = typename std::conditional<BF, __nv_bfloat16, float>::type;
+constexpr int kBatch = 4;   // rows per step
+constexpr int kDepth = 4;   // steps in a thread's ring: three in flight, one in use
+static_assert(kConvRun % kBatch == 0, "whole steps");
 
-// V elements at p (V * element size aligned) as fp32, and back.
-template <bool BF, int V>
-__device__ __forceinline__ void load_vec(const void* base, int64_t i, float (&v)[V])
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
 {
-    const InT<BF>* p = reinterpret_cast<const InT<BF>*>(base) + i;
-    if constexpr (V == 1) {
-        if constexpr (BF) v[0] = __bfloat162float(p[0]);
-        else v[0] = p[0];
-    } else if constexpr (BF) {
-        static_assert(V == 8, "16 bytes");
-        const uint4 r = *reinterpret_cast<const uint4*>(p);
-        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(u[j] << 16);
-            v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-        }
-    } else {
-        static_assert(V == 4, "16 bytes");
-        const float4 r = *reinterpret_cast<const float4*>(p);
-        v[0] = r.x;
-        v[1] = r.y;
-        v[2] = r.z;
-        v[3] = r.w;
-    }
-}
-
-template <bool BF, int V>
-__device__ __forceinline__ void store_vec(void* base, int64_t i, const float (&v)[V])
-{
-    InT<BF>* p = reinterpret_cast<InT<BF>*>(base) + i;
-    if constexpr (V == 1) {
-        if constexpr (BF) p[0] = __float2bfloat16_rn(v[0]);
-        else p[0] = v[0];
-    } else if constexpr (BF) {
-        uint32_t u[V / 2];
-#pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-            u[j] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-        else *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-    }
-}
-
-// SiLU.  For a bf16 result the hardware's exp2 and reciprocal are enough (their relative error
-// of about 2^-21 is far below bf16's 2^-9); an fp32 result takes the accurate forms.
-template <bool FAST>
-__device__ __forceinline__ float silu(float v)
-{
-    if constexpr (FAST) return __fdividef(v, 1.0f + __expf(-v));
-    else return v / (1.0f + expf(-v));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <int W, int V, bool IB, bool OB>
@@ -90,47 +40,85 @@ __global__ void __launch_bounds__(128) k_conv(ConvParams p, int ncv, int64_t wor
     if (p.lengths) len = min(max(p.lengths[b], 0), p.T);
     if (t0 >= len && t0 > 0) return;
     const int t1 = min(t0 + kConvRun, len);
+    constexpr int H = (V + 1) / 2;  // pairs of channels
 
-    float wt[V][W], bias[V], win[W][V];
+    F2 wt[W][H], bias[H], win[W + kBatch - 1][H];
+    {
+        float wv[V][W], bv[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+        for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int k = 0; k < W; ++k) wt[v][k] = p.w[static_cast<int64_t>(c + v) * W + k];
-        bias[v] = p.bias ? p.bias[c + v] : 0.0f;
+            for (int k = 0; k < W; ++k) wv[v][k] = p.w[static_cast<int64_t>(c + v) * W + k];
+            bv[v] = p.bias ? p.bias[c + v] : 0.0f;
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) wt[k][h] = f2(wv[2 * h][k], V > 1 ? wv[(2 * h + 1) % V][k] : 0.0f);
+            bias[h] = f2(bv[2 * h], V > 1 ? bv[(2 * h + 1) % V] : 0.0f);
+        }
     }
     const int64_t xb = static_cast<int64_t>(b) * p.sb + c;
     const int64_t sbase = static_cast<int64_t>(b) * (W - 1) * p.C + c;
-    float old[W - 1][V];  // the carried state, kept by the first run (it also writes state_out)
+    Raw<IB, V> old[W - 1];  // the carried state, kept by the first run (it also writes state_out)
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
         const int t = t0 - (W - 1) + k;
-        if (t >= 0) {
-            load_vec<IB, V>(p.x, xb + static_cast<int64_t>(t) * p.st, win[k]);
-        } else if (p.state_in) {
-            load_vec<IB, V>(p.state_in, sbase + static_cast<int64_t>(t + W - 1) * p.C, win[k]);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[k][v] = 0.0f;
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) old[k][v] = win[k][v];
+        if (t >= 0) old[k].load(p.x, xb + static_cast<int64_t>(t) * p.st);
+        else if (p.state_in) old[k].load(p.state_in, sbase + static_cast<int64_t>(t + W - 1) * p.C);
+        else old[k].clear();
+        old[k].widen(win[k]);
     }
-#pragma unroll 4
-    for (int t = t0; t < t1; ++t) {
-        load_vec<IB, V>(p.x, xb + static_cast<int64_t>(t) * p.st, win[W - 1]);
-        float acc[V];
+    // each thread's own ring of rows in shared memory, or (single values) one step in registers
+    __shared__ uint4 ring[V > 1 ? kDepth * kBatch * 128 : 1];
+    const uint32_t mine = smem_addr(ring + (V > 1 ? threadIdx.x : 0));
+    Raw<IB, V> next[kBatch];
+    const unsigned char* src = reinterpret_cast<const unsigned char*>(p.x) + (xb + static_cast<int64_t>(t0) * p.st) * (IB ? 2 : 4);
+    const int64_t stride = p.st * (IB ? 2 : 4);
+    auto fetch = [&](int t) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            acc[v] = bias[v];
+        for (int i = 0; i < kBatch; ++i)
+            if (t + i < t1) {
+                if constexpr (V > 1) copy16(mine + ((((t - t0) & (kDepth * kBatch - 1)) + i) << 11), src + (t - t0 + i) * stride);
+                else next[i].load(p.x, xb + static_cast<int64_t>(t + i) * p.st);
+            }
+        if constexpr (V > 1) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 #pragma unroll
-            for (int k = 0; k < W; ++k) acc[v] = fmaf(wt[v][k], win[k][v], acc[v]);
-            if (p.silu) acc[v] = silu<OB>(acc[v]);
+    for (int d = 0; d < (V > 1 ? kDepth - 1 : 1); ++d) fetch(t0 + d * kBatch);
+#pragma unroll 1
+    for (int t = t0; t < t1; t += kBatch) {
+        if constexpr (V > 1) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const uint4 v = ring[(((t - t0) & (kDepth * kBatch - 1)) + i) * 128 + threadIdx.x];
+                next[i].set(v);
+            }
         }
-        store_vec<OB, V>(p.y, (static_cast<int64_t>(b) * p.T + t) * p.C + c, acc);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) next[i].widen(win[W - 1 + i]);
+        fetch(t + (V > 1 ? (kDepth - 1) * kBatch : kBatch));
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            float y[V];
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                F2 acc = bias[h];
+#pragma unroll
+                for (int k = 0; k < W; ++k) acc = fma2(wt[k][h], win[i + k][h], acc);
+                if (p.silu) acc = silu2<OB>(acc);
+                float lo, hi;
+                un(acc, lo, hi);
+                y[2 * h] = lo;
+                if (V > 1) y[(2 * h + 1) % V] = hi;
+            }
+            if (t + i < t1) store_vec<OB, V>(p.y, (static_cast<int64_t>(b) * p.T + t + i) * p.C + c, y);
+        }
 #pragma unroll
         for (int k = 0; k < W - 1; ++k)
 #pragma unroll
-            for (int v = 0; v < V; ++v) win[k][v] = win[k + 1][v];
+            for (int h = 0; h < H; ++h) win[k][h] = win[kBatch + k][h];
     }
     // The last W-1 inputs: from x, or from the old state where the sequence is shorter.  Only
     // the first run touches the state, after it has read all of it, so it may be in place.
@@ -138,20 +126,16 @@ __global__ void __launch_bounds__(128) k_conv(ConvParams p, int ncv, int64_t wor
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
             const int t = len - (W - 1) + k;
-            float v8[V];
+            Raw<IB, V> r;
+            r.clear();
             if (t >= 0) {
-                load_vec<IB, V>(p.x, xb + static_cast<int64_t>(t) * p.st, v8);
+                r.load(p.x, xb + static_cast<int64_t>(t) * p.st);
             } else {
 #pragma unroll
-                for (int v = 0; v < V; ++v) v8[v] = 0.0f;
-#pragma unroll
                 for (int q = 0; q < W - 1; ++q)
-                    if (q == t + W - 1) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) v8[v] = old[q][v];
-                    }
+                    if (q == t + W - 1) r = old[q];
             }
-            store_vec<IB, V>(p.state_out, sbase + static_cast<int64_t>(k) * p.C, v8);
+            r.store(p.state_out, sbase + static_cast<int64_t>(k) * p.C);
         }
     }
 }
@@ -164,20 +148,31 @@ __global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p, int ncv, in
     const int c = static_cast<int>(id % ncv) * V;
     const int64_t b = id / ncv;
     const int64_t sbase = b * (W - 1) * p.C + c;
-    float win[W][V], acc[V];
+    Raw<IB, V> in[W];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) load_vec<IB, V>(p.state, sbase + static_cast<int64_t>(k) * p.C, win[k]);
-    load_vec<IB, V>(p.x, b * p.sb + c, win[W - 1]);
+    for (int k = 0; k < W - 1; ++k) in[k].load(p.state, sbase + static_cast<int64_t>(k) * p.C);
+    in[W - 1].load(p.x, b * p.sb + c);
+    constexpr int H = (V + 1) / 2;
+    F2 win[W][H];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        acc[v] = p.bias ? p.bias[c + v] : 0.0f;
+    for (int k = 0; k < W; ++k) in[k].widen(win[k]);
+    float y[V];
 #pragma unroll
-        for (int k = 0; k < W; ++k) acc[v] = fmaf(p.w[static_cast<int64_t>(c + v) * W + k], win[k][v], acc[v]);
-        if (p.silu) acc[v] = silu<OB>(acc[v]);
+    for (int h = 0; h < H; ++h) {
+        const int c1 = c + (V > 1 ? 2 * h + 1 : 0);
+        F2 acc = p.bias ? f2(p.bias[c + 2 * h], p.bias[c1]) : f2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            acc = fma2(f2(p.w[static_cast<int64_t>(c + 2 * h) * W + k], p.w[static_cast<int64_t>(c1) * W + k]), win[k][h], acc);
+        if (p.silu) acc = silu2<OB>(acc);
+        float lo, hi;
+        un(acc, lo, hi);
+        y[2 * h] = lo;
+        if (V > 1) y[(2 * h + 1) % V] = hi;
     }
-    store_vec<OB, V>(p.y, b * p.C + c, acc);
+    store_vec<OB, V>(p.y, b * p.C + c, y);
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) store_vec<IB, V>(p.state, sbase + static_cast<int64_t>(k) * p.C, win[k + 1]);
+    for (int k = 0; k < W - 1; ++k) in[k + 1].store(p.state, sbase + static_cast<int64_t>(k) * p.C);
 }
 
 bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

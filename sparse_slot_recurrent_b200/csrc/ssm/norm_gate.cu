@@ -4,103 +4,117 @@
 //   norm first:  y = x / sqrt(mean_group(x^2) + eps) * w * silu(z)
 // without z the gate is left out.  Sums in fp32, in a fixed order.
 //
-// Bound: HBM, x and z read once and y written once.  A block (or one warp, for short groups)
-// owns one group of one row and keeps it in registers between the sum and the scaling.
-#include "../common.cuh"
-#include "ssm.h"
+// Bound: HBM, x and z read once and y written once.  k_norm_warp: one warp per group of one row,
+// with all of the group's loads in flight before the first is used and no barrier (groups up to
+// 256 16-byte vectors: 2048 bf16 or 1024 fp32 channels).  k_norm_block: one block per group, for longer groups and for rows
+// that do not start on 16 bytes; what it does not keep in registers it reads again, from L2.
+// (One block per row for all: 229 us for 65536 x 2048 bf16 rows, the block's barrier and its few
+// bytes in flight.)
+#include "rows.cuh"
 
 namespace ramnet {
 namespace {
 
-template <bool BF, int V>
-__device__ __forceinline__ void load_vec(const void* base, int64_t i, float (&v)[V])
+// PRE: the gate, if any, comes before the norm (z is then used up before the sum).
+template <int V, int NV, bool IB, bool OB, bool PRE>
+__global__ void __launch_bounds__(128, 4) k_norm_warp(NormParams p)
 {
-    if constexpr (V == 1) {
-        v[0] = load_in(base, static_cast<size_t>(i), BF);
-    } else if constexpr (BF) {
-        const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(base) + i);
-        const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (id >= p.R * p.groups) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t row = id / p.groups;
+    const int width = p.D / p.groups, first = static_cast<int>(id % p.groups) * width, nv = width / V;
+    Raw<IB, V> x[NV], z[NV];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(u[j] << 16);
-            v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+    for (int k = 0; k < NV; ++k) {
+        x[k].clear();
+        z[k].clear();
+        const int i = lane + 32 * k;
+        if (i < nv) {
+            x[k].load(p.x, row * p.sx + first + static_cast<int64_t>(i) * V);
+            if (p.z) z[k].load(p.z, row * p.sz + first + static_cast<int64_t>(i) * V);
         }
-    } else {
-        load_row_g<V>(reinterpret_cast<const float*>(base) + i, v);
     }
-}
-
-template <bool BF, int V>
-__device__ __forceinline__ void store_vec(void* base, int64_t i, const float (&v)[V])
-{
-    if constexpr (V == 1) {
-        store_out(base, static_cast<size_t>(i), v[0], BF);
-    } else if constexpr (BF) {
-        uint32_t u[V / 2];
+    const bool pre = PRE && p.z;
+    F2 u[NV][V / 2], sum2 = f2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-            u[j] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int h = 0; h < V / 2; ++h) {
+            u[k][h] = x[k].pair(h);
+            if (pre) u[k][h] = mul2(u[k][h], silu2<OB>(z[k].pair(h)));
+            sum2 = fma2(u[k][h], u[k][h], sum2);
         }
-        uint32_t* p = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(base) + i);
-        if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-        else *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
-    } else {
-        store_row_g<V>(reinterpret_cast<float*>(base) + i, v);
+    float sum, other;
+    un(sum2, sum, other);
+    sum += other;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = 1.0f / sqrtf(sum / static_cast<float>(width) + p.eps);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = lane + 32 * k, d = first + i * V;
+        if (i < nv) {
+            float y[V];
+#pragma unroll
+            for (int h = 0; h < V / 2; ++h) {
+                F2 v = mul2(u[k][h], f2(inv, inv));
+                if (p.w) {
+                    const float2 w = *reinterpret_cast<const float2*>(p.w + d + 2 * h);
+                    v = mul2(v, f2(w.x, w.y));
+                }
+                if (!PRE) v = mul2(v, silu2<OB>(z[k].pair(h)));
+                un(v, y[2 * h], y[2 * h + 1]);
+            }
+            store_vec<OB, V>(p.y, row * p.D + d, y);
+        }
     }
-}
-
-// as in the convolution: the hardware's exp2 and reciprocal where the result is bf16
-template <bool FAST>
-__device__ __forceinline__ float silu(float v)
-{
-    if constexpr (FAST) return __fdividef(v, 1.0f + __expf(-v));
-    else return v / (1.0f + expf(-v));
 }
 
 constexpr int kThreads = 256;
 
-// One group of one row per block; each thread keeps up to NV vectors of V channels, a longer
-// group is read a second time (from L2) for the scaling.
+// One group of one row per block; each thread keeps up to NV vectors of V channels.
 template <int V, int NV, bool IB, bool OB>
-__global__ void __launch_bounds__(kThreads) k_norm_gate(NormParams p)
+__global__ void __launch_bounds__(kThreads) k_norm_block(NormParams p)
 {
     __shared__ float part[kThreads / 32];
+    constexpr int H = (V + 1) / 2;
     const int64_t row = blockIdx.x / p.groups;
-    const int g = static_cast<int>(blockIdx.x % p.groups);
-    const int width = p.D / p.groups;
-    const int64_t xo = row * p.sx + static_cast<int64_t>(g) * width;
-    const int64_t zo = row * p.sz + static_cast<int64_t>(g) * width;
-    const int nv = width / V;
-    float u[NV][V], gate[NV][V];
+    const int width = p.D / p.groups, first = static_cast<int>(blockIdx.x % p.groups) * width, nv = width / V;
+    F2 u[NV][H], gate[NV][H];
 
-    auto fetch = [&](int i, float (&uu)[V], float (&gg)[V]) {
-        load_vec<IB, V>(p.x, xo + static_cast<int64_t>(i) * V, uu);
+    auto fetch = [&](int i, F2 (&uu)[H], F2 (&gg)[H]) {
+        Raw<IB, V> x, z;
+        x.load(p.x, row * p.sx + first + static_cast<int64_t>(i) * V);
+        x.widen(uu);
         if (p.z) {
-            load_vec<IB, V>(p.z, zo + static_cast<int64_t>(i) * V, gg);
+            z.load(p.z, row * p.sz + first + static_cast<int64_t>(i) * V);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                gg[v] = silu<OB>(gg[v]);
-                if (p.gate_first) uu[v] *= gg[v];
+            for (int h = 0; h < H; ++h) {
+                gg[h] = silu2<OB>(z.pair(h));
+                if (p.gate_first) uu[h] = mul2(uu[h], gg[h]);
             }
         }
     };
-    float sum = 0.0f;
+    F2 sum2 = f2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int i = threadIdx.x + k * kThreads;
         if (i < nv) {
             fetch(i, u[k], gate[k]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) sum = fmaf(u[k][v], u[k][v], sum);
+            for (int h = 0; h < H; ++h) sum2 = fma2(u[k][h], u[k][h], sum2);
         }
     }
     for (int i = threadIdx.x + NV * kThreads; i < nv; i += kThreads) {
-        float uu[V], gg[V];
+        F2 uu[H], gg[H];
         fetch(i, uu, gg);
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum = fmaf(uu[v], uu[v], sum);
+        for (int h = 0; h < H; ++h) sum2 = fma2(uu[h], uu[h], sum2);
     }
+    float sum, other;
+    un(sum2, sum, other);
+    sum += other;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
@@ -110,17 +124,20 @@ __global__ void __launch_bounds__(kThreads) k_norm_gate(NormParams p)
     for (int i = 1; i < kThreads / 32; ++i) sum += part[i];
     const float inv = 1.0f / sqrtf(sum / static_cast<float>(width) + p.eps);
 
-    auto finish = [&](int i, float (&uu)[V], float (&gg)[V]) {
-        const int d = g * width + i * V;
-        float wv[V];
-        if (p.w) load_vec<false, V == 8 ? 8 : V>(p.w, d, wv);
+    auto finish = [&](int i, const F2 (&uu)[H], const F2 (&gg)[H]) {
+        const int d = first + i * V;
+        float y[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            uu[v] *= inv;
-            if (p.w) uu[v] *= wv[v];
-            if (p.z && !p.gate_first) uu[v] *= gg[v];
+        for (int h = 0; h < H; ++h) {
+            F2 v = mul2(uu[h], f2(inv, inv));
+            if (p.w) v = mul2(v, f2(p.w[d + 2 * h], p.w[d + (V > 1 ? 2 * h + 1 : 0)]));
+            if (p.z && !p.gate_first) v = mul2(v, gg[h]);
+            float lo, hi;
+            un(v, lo, hi);
+            y[2 * h] = lo;
+            if (V > 1) y[(2 * h + 1) % V] = hi;
         }
-        store_vec<OB, V>(p.y, row * p.D + d, uu);
+        store_vec<OB, V>(p.y, row * p.D + d, y);
     };
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -128,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_gate(NormParams p)
         if (i < nv) finish(i, u[k], gate[k]);
     }
     for (int i = threadIdx.x + NV * kThreads; i < nv; i += kThreads) {
-        float uu[V], gg[V];
+        F2 uu[H], gg[H];
         fetch(i, uu, gg);
         finish(i, uu, gg);
     }
@@ -137,12 +154,32 @@ __global__ void __launch_bounds__(kThreads) k_norm_gate(NormParams p)
 bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 template <int V, int NV, bool IB>
-cudaError_t go(const NormParams& p, cudaStream_t s)
+cudaError_t block(const NormParams& p, cudaStream_t s)
 {
     const unsigned grid = static_cast<unsigned>(p.R * p.groups);
-    if (p.out_bf16) k_norm_gate<V, NV, IB, true><<<grid, kThreads, 0, s>>>(p);
-    else k_norm_gate<V, NV, IB, false><<<grid, kThreads, 0, s>>>(p);
+    if (p.out_bf16) k_norm_block<V, NV, IB, true><<<grid, kThreads, 0, s>>>(p);
+    else k_norm_block<V, NV, IB, false><<<grid, kThreads, 0, s>>>(p);
     return cudaGetLastError();
+}
+
+template <int V, int NV, bool IB>
+cudaError_t warp(const NormParams& p, cudaStream_t s)
+{
+    const unsigned grid = static_cast<unsigned>((p.R * p.groups + 3) / 4);
+    const bool pre = p.gate_first || !p.z;
+    if (p.out_bf16) pre ? k_norm_warp<V, NV, IB, true, true><<<grid, 128, 0, s>>>(p) : k_norm_warp<V, NV, IB, true, false><<<grid, 128, 0, s>>>(p);
+    else pre ? k_norm_warp<V, NV, IB, false, true><<<grid, 128, 0, s>>>(p) : k_norm_warp<V, NV, IB, false, false><<<grid, 128, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+template <int V, bool IB>
+cudaError_t pick(const NormParams& p, int nv, cudaStream_t s)
+{
+    if (nv <= 32) return warp<V, 1, IB>(p, s);
+    if (nv <= 64) return warp<V, 2, IB>(p, s);
+    if (nv <= 128) return warp<V, 4, IB>(p, s);
+    if (nv <= 256) return warp<V, 8, IB>(p, s);
+    return block<V, 2, IB>(p, s);
 }
 
 }  // namespace
@@ -152,8 +189,8 @@ cudaError_t launch_norm_gate(const NormParams& p, cudaStream_t s)
     const int v = p.in_bf16 ? 8 : 4;
     const int width = p.D / p.groups;
     const bool vec = width % v == 0 && p.sx % v == 0 && al(p.x, 16) && (!p.z || (p.sz % v == 0 && al(p.z, 16)));
-    if (p.in_bf16) return vec ? go<8, 2, true>(p, s) : go<1, 4, true>(p, s);
-    return vec ? go<4, 2, false>(p, s) : go<1, 4, false>(p, s);
+    if (p.in_bf16) return vec ? pick<8, true>(p, width / 8, s) : block<1, 4, true>(p, s);
+    return vec ? pick<4, false>(p, width / 4, s) : block<1, 4, false>(p, s);
 }
 
 }  // namespace ramnet

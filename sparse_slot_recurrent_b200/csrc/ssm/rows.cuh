@@ -1,0 +1,98 @@
+// rows.cuh -- device helpers of the kernels that stream rows of channels: pairs of fp32, vectors of V
+// neighbouring values (16 bytes, or one value where addresses do not allow that), SiLU.
+#pragma once
+
+#include "../common.cuh"
+#include "pairs.cuh"
+#include "ssm.h"
+
+namespace ramnet {
+namespace {
+
+// V values as they lie in memory, bf16 (BF) or fp32; V is 1 or fills 16 bytes.
+template <bool BF, int V>
+struct Raw {
+    static constexpr int kWords = V == 1 ? 1 : 4;
+    uint32_t r[kWords];
+
+    __device__ __forceinline__ void load(const void* base, int64_t i)
+    {
+        if constexpr (V == 1) {
+            if constexpr (BF) r[0] = reinterpret_cast<const uint16_t*>(base)[i];
+            else r[0] = reinterpret_cast<const uint32_t*>(base)[i];
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(base) + i * (16 / V));
+            r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+        }
+    }
+    __device__ __forceinline__ void store(void* base, int64_t i) const
+    {
+        if constexpr (V == 1) {
+            if constexpr (BF) reinterpret_cast<uint16_t*>(base)[i] = static_cast<uint16_t>(r[0]);
+            else reinterpret_cast<uint32_t*>(base)[i] = r[0];
+        } else {
+            *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(base) + i * (16 / V)) = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+    }
+    __device__ __forceinline__ void set(uint4 v)
+    {
+        static_assert(V > 1, "16 bytes");
+        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+    }
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) r[k] = 0;
+    }
+    __device__ __forceinline__ F2 pair(int h) const  // values 2h and 2h+1 (a lone value with 0 behind it)
+    {
+        if constexpr (V == 1) return f2(BF ? bf_lo(r[0]) : __uint_as_float(r[0]), 0.0f);
+        else if constexpr (BF) return bf_pair(r[h]);
+        else return f2(__uint_as_float(r[2 * h]), __uint_as_float(r[2 * h + 1]));
+    }
+    __device__ __forceinline__ void widen(F2 (&p)[(V + 1) / 2]) const
+    {
+#pragma unroll
+        for (int h = 0; h < (V + 1) / 2; ++h) p[h] = pair(h);
+    }
+};
+
+template <bool BF, int V>
+__device__ __forceinline__ void store_vec(void* base, int64_t i, const float (&v)[V])
+{
+    if constexpr (V == 1) {
+        store_out(base, static_cast<size_t>(i), v[0], BF);
+    } else if constexpr (BF) {
+        uint32_t u[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) u[j] = pack_rn(f2(v[2 * j], v[2 * j + 1]));
+        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(base) + i;
+        if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        else *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+    } else {
+        store_row_g<V>(reinterpret_cast<float*>(base) + i, v);
+    }
+}
+
+// SiLU.  For a bf16 result the hardware's exp2 and reciprocal are enough (their relative error
+// of about 2^-21 is far below bf16's 2^-9); an fp32 result takes the accurate forms.
+template <bool FAST>
+__device__ __forceinline__ F2 silu2(F2 p)
+{
+    float a, b;
+    if constexpr (FAST) {
+        un(mul2(p, f2(-1.44269504f, -1.44269504f)), a, b);
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+        asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+        un(add2(f2(a, b), f2(1.0f, 1.0f)), a, b);
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+        asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+        return mul2(p, f2(a, b));
+    } else {
+        un(p, a, b);
+        return f2(a / (1.0f + expf(-a)), b / (1.0f + expf(-b)));
+    }
+}
+
+}  // namespace
+}  // namespace ramnet
