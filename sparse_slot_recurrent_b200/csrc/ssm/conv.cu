@@ -7,18 +7,18 @@
 // neighbouring channels (16 bytes where addresses allow) over a run of tokens and slides a
 // window of W-1 inputs in registers, so each input is read once but for W-1 rows per run (which
 // the run before has just brought into L2).  Rows come through a ring in shared memory that
-// only its own thread fills and reads, up to twelve in flight (for 4 x 16384 x 2304 bf16 channels: 273 us with one
-// load at a time behind the store before it, 209 us with four in registers).  Products and sums run on pairs of channels.
+// only its own thread fills and reads, up to fourteen in flight.  For 4 x 16384 x 2304 bf16 channels: 273 us with one
+// load at a time behind the store before it, 209 us with four in registers, 119 us this way (77% of the copy
+// bandwidth); a fifth block per SM would cost the registers of the weights (185 us).  Products and sums run on pairs of channels.
 #include "rows.cuh"
 
 namespace ramnet {
 namespace {
 
-constexpr int kConvRun = 32;  // tokens per thread
+constexpr int kRunShort = 16, kRunLong = 64;  // tokens per thread
 
-constexpr int kBatch = 4;   // rows per step
-constexpr int kDepth = 4;   // steps in a thread's ring: three in flight, one in use
-static_assert(kConvRun % kBatch == 0, "whole steps");
+constexpr int kDepth = 8;   // steps of two rows in a thread's ring: seven in flight, one in use
+static_assert(kRunShort % 8 == 0 && kRunLong % 8 == 0, "whole steps");
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
 {
@@ -26,36 +26,45 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src)
 }
 
 template <int W, int V, bool IB, bool OB>
-__global__ void __launch_bounds__(128) k_conv(ConvParams p, int ncv, int64_t work)
+__global__ void __launch_bounds__(128, V > 1 ? 4 : 1) k_conv(ConvParams p, int ncv, int64_t work, int run_len)
 {
     const int64_t id = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
     if (id >= work) return;
     const int cv = static_cast<int>(id % ncv);
     const int64_t run = id / ncv;
-    const int runs = (p.T + kConvRun - 1) / kConvRun;
+    const int runs = (p.T + run_len - 1) / run_len;
     const int b = static_cast<int>(run / runs);
-    const int t0 = static_cast<int>(run % runs) * kConvRun;
+    const int t0 = static_cast<int>(run % runs) * run_len;
     const int c = cv * V;
     int len = p.T;
     if (p.lengths) len = min(max(p.lengths[b], 0), p.T);
     if (t0 >= len && t0 > 0) return;
-    const int t1 = min(t0 + kConvRun, len);
-    constexpr int H = (V + 1) / 2;  // pairs of channels
+    const int t1 = min(t0 + run_len, len);
+    constexpr int H = (V + 1) / 2;            // pairs of channels
+    constexpr int kBatch = V > 1 ? 2 : 8;     // rows per step (single values: in registers)
 
-    F2 wt[W][H], bias[H], win[W + kBatch - 1][H];
+    Val<V> wt[W][H], bias[H], win[W + kBatch - 1][H];
     {
         float wv[V][W], bv[V];
+        const bool wide = W == 4 && (reinterpret_cast<uintptr_t>(p.w) & 15) == 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            if (wide) {
+                const float4 f = *reinterpret_cast<const float4*>(p.w + static_cast<int64_t>(c + v) * 4);
+                const float a[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int k = 0; k < W; ++k) wv[v][k] = p.w[static_cast<int64_t>(c + v) * W + k];
+                for (int k = 0; k < W; ++k) wv[v][k] = a[k];
+            } else {
+#pragma unroll
+                for (int k = 0; k < W; ++k) wv[v][k] = p.w[static_cast<int64_t>(c + v) * W + k];
+            }
             bv[v] = p.bias ? p.bias[c + v] : 0.0f;
         }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
 #pragma unroll
-            for (int k = 0; k < W; ++k) wt[k][h] = f2(wv[2 * h][k], V > 1 ? wv[(2 * h + 1) % V][k] : 0.0f);
-            bias[h] = f2(bv[2 * h], V > 1 ? bv[(2 * h + 1) % V] : 0.0f);
+            for (int k = 0; k < W; ++k) wt[k][h] = val<V>(wv[2 * h][k], wv[(2 * h + 1) % V][k]);
+            bias[h] = val<V>(bv[2 * h], bv[(2 * h + 1) % V]);
         }
     }
     const int64_t xb = static_cast<int64_t>(b) * p.sb + c;
@@ -104,14 +113,11 @@ __global__ void __launch_bounds__(128) k_conv(ConvParams p, int ncv, int64_t wor
             float y[V];
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                F2 acc = bias[h];
+                Val<V> acc = bias[h];
 #pragma unroll
                 for (int k = 0; k < W; ++k) acc = fma2(wt[k][h], win[i + k][h], acc);
                 if (p.silu) acc = silu2<OB>(acc);
-                float lo, hi;
-                un(acc, lo, hi);
-                y[2 * h] = lo;
-                if (V > 1) y[(2 * h + 1) % V] = hi;
+                put<V>(acc, h, y);
             }
             if (t + i < t1) store_vec<OB, V>(p.y, (static_cast<int64_t>(b) * p.T + t + i) * p.C + c, y);
         }
@@ -153,22 +159,19 @@ __global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p, int ncv, in
     for (int k = 0; k < W - 1; ++k) in[k].load(p.state, sbase + static_cast<int64_t>(k) * p.C);
     in[W - 1].load(p.x, b * p.sb + c);
     constexpr int H = (V + 1) / 2;
-    F2 win[W][H];
+    Val<V> win[W][H];
 #pragma unroll
     for (int k = 0; k < W; ++k) in[k].widen(win[k]);
     float y[V];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
         const int c1 = c + (V > 1 ? 2 * h + 1 : 0);
-        F2 acc = p.bias ? f2(p.bias[c + 2 * h], p.bias[c1]) : f2(0.0f, 0.0f);
+        Val<V> acc = p.bias ? val<V>(p.bias[c + 2 * h], p.bias[c1]) : val<V>(0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < W; ++k)
-            acc = fma2(f2(p.w[static_cast<int64_t>(c + 2 * h) * W + k], p.w[static_cast<int64_t>(c1) * W + k]), win[k][h], acc);
+            acc = fma2(val<V>(p.w[static_cast<int64_t>(c + 2 * h) * W + k], p.w[static_cast<int64_t>(c1) * W + k]), win[k][h], acc);
         if (p.silu) acc = silu2<OB>(acc);
-        float lo, hi;
-        un(acc, lo, hi);
-        y[2 * h] = lo;
-        if (V > 1) y[(2 * h + 1) % V] = hi;
+        put<V>(acc, h, y);
     }
     store_vec<OB, V>(p.y, b * p.C + c, y);
 #pragma unroll
@@ -181,8 +184,11 @@ template <int W, int V, bool IB, bool OB>
 cudaError_t go(const ConvParams& p, cudaStream_t s)
 {
     const int ncv = p.C / V;
-    const int64_t work = static_cast<int64_t>(ncv) * p.B * ((p.T + kConvRun - 1) / kConvRun);
-    k_conv<W, V, IB, OB><<<static_cast<unsigned>((work + 127) / 128), 128, 0, s>>>(p, ncv, work);
+    // Long runs read fewer rows twice and load their weights less often; short ones where those would leave SMs idle.
+    int run = kRunLong;
+    while (run > kRunShort && static_cast<int64_t>(ncv) * p.B * ((p.T + run - 1) / run) < 2ll * 148 * 640) run /= 2;
+    const int64_t work = static_cast<int64_t>(ncv) * p.B * ((p.T + run - 1) / run);
+    k_conv<W, V, IB, OB><<<static_cast<unsigned>((work + 127) / 128), 128, 0, s>>>(p, ncv, work, run);
     return cudaGetLastError();
 }
 

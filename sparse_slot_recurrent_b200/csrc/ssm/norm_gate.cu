@@ -81,9 +81,9 @@ __global__ void __launch_bounds__(kThreads) k_norm_block(NormParams p)
     constexpr int H = (V + 1) / 2;
     const int64_t row = blockIdx.x / p.groups;
     const int width = p.D / p.groups, first = static_cast<int>(blockIdx.x % p.groups) * width, nv = width / V;
-    F2 u[NV][H], gate[NV][H];
+    Val<V> u[NV][H], gate[NV][H];
 
-    auto fetch = [&](int i, F2 (&uu)[H], F2 (&gg)[H]) {
+    auto fetch = [&](int i, Val<V> (&uu)[H], Val<V> (&gg)[H]) {
         Raw<IB, V> x, z;
         x.load(p.x, row * p.sx + first + static_cast<int64_t>(i) * V);
         x.widen(uu);
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_block(NormParams p)
             }
         }
     };
-    F2 sum2 = f2(0.0f, 0.0f);
+    Val<V> sum2 = val<V>(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int i = threadIdx.x + k * kThreads;
@@ -107,14 +107,14 @@ __global__ void __launch_bounds__(kThreads) k_norm_block(NormParams p)
         }
     }
     for (int i = threadIdx.x + NV * kThreads; i < nv; i += kThreads) {
-        F2 uu[H], gg[H];
+        Val<V> uu[H], gg[H];
         fetch(i, uu, gg);
 #pragma unroll
         for (int h = 0; h < H; ++h) sum2 = fma2(uu[h], uu[h], sum2);
     }
-    float sum, other;
-    un(sum2, sum, other);
-    sum += other;
+    float both[V > 1 ? V : 1] = {};
+    put<V>(sum2, 0, both);
+    float sum = both[0] + (V > 1 ? both[V > 1 ? 1 : 0] : 0.0f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
@@ -124,18 +124,15 @@ __global__ void __launch_bounds__(kThreads) k_norm_block(NormParams p)
     for (int i = 1; i < kThreads / 32; ++i) sum += part[i];
     const float inv = 1.0f / sqrtf(sum / static_cast<float>(width) + p.eps);
 
-    auto finish = [&](int i, const F2 (&uu)[H], const F2 (&gg)[H]) {
+    auto finish = [&](int i, const Val<V> (&uu)[H], const Val<V> (&gg)[H]) {
         const int d = first + i * V;
         float y[V];
 #pragma unroll
         for (int h = 0; h < H; ++h) {
-            F2 v = mul2(uu[h], f2(inv, inv));
-            if (p.w) v = mul2(v, f2(p.w[d + 2 * h], p.w[d + (V > 1 ? 2 * h + 1 : 0)]));
+            Val<V> v = mul2(uu[h], val<V>(inv, inv));
+            if (p.w) v = mul2(v, val<V>(p.w[d + 2 * h], p.w[d + (V > 1 ? 2 * h + 1 : 0)]));
             if (p.z && !p.gate_first) v = mul2(v, gg[h]);
-            float lo, hi;
-            un(v, lo, hi);
-            y[2 * h] = lo;
-            if (V > 1) y[(2 * h + 1) % V] = hi;
+            put<V>(v, h, y);
         }
         store_vec<OB, V>(p.y, row * p.D + d, y);
     };
@@ -145,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_block(NormParams p)
         if (i < nv) finish(i, u[k], gate[k]);
     }
     for (int i = threadIdx.x + NV * kThreads; i < nv; i += kThreads) {
-        F2 uu[H], gg[H];
+        Val<V> uu[H], gg[H];
         fetch(i, uu, gg);
         finish(i, uu, gg);
     }

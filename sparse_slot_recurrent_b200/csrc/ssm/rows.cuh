@@ -2,12 +2,32 @@
 // neighbouring values (16 bytes, or one value where addresses do not allow that), SiLU.
 #pragma once
 
+#include <type_traits>
+
 #include "../common.cuh"
 #include "pairs.cuh"
 #include "ssm.h"
 
 namespace ramnet {
 namespace {
+
+// What one step of arithmetic works on: a pair of values, or a lone one.
+template <int V>
+using Val = typename std::conditional<V == 1, float, F2>::type;
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+template <int V>
+__device__ __forceinline__ Val<V> val(float a, float b)
+{
+    if constexpr (V == 1) return a;
+    else return f2(a, b);
+}
+template <int V>
+__device__ __forceinline__ void put(Val<V> p, int h, float (&y)[V])
+{
+    if constexpr (V == 1) y[0] = p;
+    else un(p, y[2 * h], y[2 * h + 1]);
+}
 
 // V values as they lie in memory, bf16 (BF) or fp32; V is 1 or fills 16 bytes.
 template <bool BF, int V>
@@ -44,13 +64,13 @@ struct Raw {
 #pragma unroll
         for (int k = 0; k < kWords; ++k) r[k] = 0;
     }
-    __device__ __forceinline__ F2 pair(int h) const  // values 2h and 2h+1 (a lone value with 0 behind it)
+    __device__ __forceinline__ Val<V> pair(int h) const  // values 2h and 2h+1
     {
-        if constexpr (V == 1) return f2(BF ? bf_lo(r[0]) : __uint_as_float(r[0]), 0.0f);
+        if constexpr (V == 1) return BF ? bf_lo(r[0]) : __uint_as_float(r[0]);
         else if constexpr (BF) return bf_pair(r[h]);
         else return f2(__uint_as_float(r[2 * h]), __uint_as_float(r[2 * h + 1]));
     }
-    __device__ __forceinline__ void widen(F2 (&p)[(V + 1) / 2]) const
+    __device__ __forceinline__ void widen(Val<V> (&p)[(V + 1) / 2]) const
     {
 #pragma unroll
         for (int h = 0; h < (V + 1) / 2; ++h) p[h] = pair(h);
@@ -92,6 +112,13 @@ __device__ __forceinline__ F2 silu2(F2 p)
         un(p, a, b);
         return f2(a / (1.0f + expf(-a)), b / (1.0f + expf(-b)));
     }
+}
+
+template <bool FAST>
+__device__ __forceinline__ float silu2(float a)
+{
+    if constexpr (FAST) return __fdividef(a, 1.0f + __expf(-a));
+    else return a / (1.0f + expf(-a));
 }
 
 }  // namespace

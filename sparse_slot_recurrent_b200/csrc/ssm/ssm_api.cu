@@ -189,7 +189,7 @@ ramnet_status ramnet_conv_forward(int32_t B, int32_t T, int32_t C, int32_t W, ra
     CHECK(B >= 1 && T >= 1 && C >= 1, "B, T, C must be >= 1");
     CHECK(static_cast<int64_t>(B) * T <= (1ll << 31) - 1 &&
               static_cast<int64_t>(B) * C <= (1ll << 31) - 1 &&
-              static_cast<double>(B) * C * ((static_cast<int64_t>(T) + 31) / 32) <= 1.0e11,
+              static_cast<double>(B) * C * ((static_cast<int64_t>(T) + 15) / 16) <= 1.0e11,
           "B*T*C too large");
     CHECK(W >= 2 && W <= 4, "W=%d outside [2,4]", W);
     CHECK(valid_dtype(in_dt) && valid_dtype(out_dt), "bad dtype");
