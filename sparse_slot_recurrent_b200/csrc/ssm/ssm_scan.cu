@@ -2,9 +2,10 @@
 // point allows), and the chaining of segments:
 //   d = clamp(softplus(dt + bias)),  S_t = exp(d A) S_{t-1} + d B_t (x) x_t,  y_t = C_t . S_t + D x_t
 //
-// k_ssm_scan: NS = N/16 neighbouring lanes own one channel p of one head and hold 16 of its N
-// state values each in registers; blocks of kTok tokens of B, C, x and the step sizes are staged
-// in shared memory.  Per token a thread takes 3 x 16 multiply-adds and a log2(NS)-step lane sum.
+// k_ssm_scan: NS neighbouring lanes own one channel p of one head and hold NR = N/NS of its state values each in
+// registers (NR = 16, fewer for small heads, so that a block has 128 threads).  Blocks of kTok tokens of B, C, x and the
+// step sizes go through shared memory; while one is worked on, the next is on its way into registers.  Per token a
+// thread takes 3 NR multiply-adds and a log2(NS)-step lane sum.
 // Bound: fp32 issue (3 N P per token-head) and, with few heads, the latency of the token chain.
 #include "ssm_common.cuh"
 
@@ -13,70 +14,83 @@ namespace {
 
 constexpr int kTok = 16;
 
-template <int N, bool OUT>
-__global__ void __launch_bounds__(128) k_ssm_scan(SsmParams p)
+template <int N, int NR, int PT, bool OUT>
+__global__ void __launch_bounds__(PT * (N / NR)) k_ssm_scan(SsmParams p)
 {
-    constexpr int NS = N / 16;
-    extern __shared__ float sm[];
-    const int pt = blockDim.x / NS;  // channels per block
-    float* sB = sm;                  // [kTok][N]
-    float* sC = sB + kTok * N;       // [kTok][N]
-    float* sX = sC + kTok * N;       // [kTok][pt]
-    float* sA = sX + kTok * pt;      // [kTok] decay
-    float* sD = sA + kTok;           // [kTok] step size
-    const int seg = blockIdx.y;
-    const int ptiles = p.P / pt;
+    constexpr int NS = N / NR, TH = PT * NS;  // lanes per channel, threads
+    constexpr int LB = kTok * N / TH, LX = (kTok * PT + TH - 1) / TH;
+    static_assert(NS <= 32 && kTok * N % TH == 0, "shape");
+    __shared__ __align__(16) float sB[kTok * N], sC[OUT ? kTok * N : 4], sX[kTok * PT], sA[kTok], sD[kTok];
+    const int seg = blockIdx.y, tid = threadIdx.x;
+    const int ptiles = p.P / PT;
     const int tile = static_cast<int>(blockIdx.x % ptiles);
     const int64_t bh = blockIdx.x / ptiles;
     const int h = static_cast<int>(bh % p.H);
     const int64_t b = bh / p.H;
     const int g = h / (p.H / p.G);
     const SegRange r = seg_range(seq_len(p.lengths, static_cast<int>(b), p.T), seg, OUT ? p.split.seg_len : p.split.piece_len());
-    const int s = threadIdx.x % NS, pl = threadIdx.x / NS;
-    const int ch = tile * pt + pl;
+    const int s = tid % NS, pl = tid / NS;
+    const int ch = tile * PT + pl;
     const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f, skip = p.D ? p.D[h] : 0.0f;
 
     // state value k of this thread is n = 4 * (s + NS * (k / 4)) + k % 4
-    float S[16];
+    float S[NR];
     const float* start = nullptr;
     if (OUT) {
         if (p.split.nseg > 1) start = p.seg_state + (bh * p.split.slots() + seg * p.split.sub) * static_cast<int64_t>(N) * p.P;
         else if (p.S_in) start = p.S_in + bh * static_cast<int64_t>(N) * p.P;
     }
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
+    for (int k = 0; k < NR; ++k) {
         const int n = 4 * (s + NS * (k / 4)) + k % 4;
         S[k] = start ? start[static_cast<int64_t>(n) * p.P + ch] : 0.0f;
     }
-    double logdecay = 0.0;
+    // the block of tokens from t0, into registers (tokens that are not there as zeros)
+    float vB[LB], vC[LB], vX[LX], vD = 0.0f;
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int k = 0; k < LB; ++k) {
+            const int i = k * TH + tid, t = t0 + i / N, n = i % N;
+            vB[k] = t < r.last ? load_in(p.Bm, static_cast<size_t>(b * p.bs.b + t * p.bs.t + g * p.bs.h + n), p.in_bf16) : 0.0f;
+            if (OUT) vC[k] = t < r.last ? load_in(p.Cm, static_cast<size_t>(b * p.cs.b + t * p.cs.t + g * p.cs.h + n), p.in_bf16) : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < LX; ++k) {
+            const int i = k * TH + tid, t = t0 + i / PT;
+            vX[k] = i < kTok * PT && t < r.last ? load_in(p.x, static_cast<size_t>(b * p.xs.b + t * p.xs.t + h * p.xs.h + tile * PT + i % PT), p.in_bf16) : 0.0f;
+        }
+        if (tid < kTok && t0 + tid < r.last) vD = load_in(p.dt, static_cast<size_t>(b * p.dts.b + (t0 + tid) * p.dts.t + h * p.dts.h), p.in_bf16);
+    };
+    double logdecay = 0.0;  // of this thread's tokens (the first kTok threads)
+    if (r.first < r.last) fetch(r.first);
     for (int t0 = r.first; t0 < r.last; t0 += kTok) {
         const int nt = min(kTok, r.last - t0);
         __syncthreads();
-        for (int i = threadIdx.x; i < nt * N; i += blockDim.x) {
-            const int t = i / N, n = i % N;
-            sB[i] = load_in(p.Bm, static_cast<size_t>(b * p.bs.b + (t0 + t) * p.bs.t + g * p.bs.h + n), p.in_bf16);
-            if (OUT) sC[i] = load_in(p.Cm, static_cast<size_t>(b * p.cs.b + (t0 + t) * p.cs.t + g * p.cs.h + n), p.in_bf16);
+#pragma unroll
+        for (int k = 0; k < LB; ++k) {
+            sB[k * TH + tid] = vB[k];
+            if (OUT) sC[k * TH + tid] = vC[k];
         }
-        for (int i = threadIdx.x; i < nt * pt; i += blockDim.x) {
-            const int t = i / pt, q = i % pt;
-            sX[i] = load_in(p.x, static_cast<size_t>(b * p.xs.b + (t0 + t) * p.xs.t + h * p.xs.h + tile * pt + q), p.in_bf16);
-        }
-        for (int t = threadIdx.x; t < nt; t += blockDim.x) {
-            const float d = step_size(load_in(p.dt, static_cast<size_t>(b * p.dts.b + (t0 + t) * p.dts.t + h * p.dts.h), p.in_bf16),
-                                      bias, p.softplus, p.dt_min, p.dt_max);
-            sD[t] = d;
+#pragma unroll
+        for (int k = 0; k < LX; ++k)
+            if (k * TH + tid < kTok * PT) sX[k * TH + tid] = vX[k];
+        if (tid < nt) {
+            const float d = step_size(vD, bias, p.softplus, p.dt_min, p.dt_max);
+            const double l = static_cast<double>(d) * A;
+            sD[tid] = d;
             // rounded once from 64 bits: a bias of expf, a fraction of an ulp, would add up over
             // the thousands of tokens that a slowly decaying state remembers
-            sA[t] = static_cast<float>(exp(static_cast<double>(d) * static_cast<double>(A)));
+            sA[tid] = exp2_of(l * 1.4426950408889634074);
+            logdecay += l;
         }
         __syncthreads();
-        if (!OUT && threadIdx.x == 0)
-            for (int t = 0; t < nt; ++t) logdecay += static_cast<double>(sD[t]) * static_cast<double>(A);
+        if (t0 + kTok < r.last) fetch(t0 + kTok);
+#pragma unroll 2
         for (int t = 0; t < nt; ++t) {
-            const float a = sA[t], x = sX[t * pt + pl], u = sD[t] * x;
+            const float a = sA[t], x = sX[t * PT + pl], u = sD[t] * x;
             float y = 0.0f;
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
+            for (int k4 = 0; k4 < NR / 4; ++k4) {
                 const float4 bv = *reinterpret_cast<const float4*>(sB + t * N + 4 * (s + NS * k4));
                 const float bb[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll
@@ -101,13 +115,17 @@ __global__ void __launch_bounds__(128) k_ssm_scan(SsmParams p)
     else if (seg == p.split.nseg - 1) end = p.S_out + bh * static_cast<int64_t>(N) * p.P;
     if (end) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < NR; ++k) {
             const int n = 4 * (s + NS * (k / 4)) + k % 4;
             end[static_cast<int64_t>(n) * p.P + ch] = S[k];
         }
     }
-    if (!OUT && threadIdx.x == 0 && tile == 0)
-        p.seg_decay[bh * p.split.pieces() + seg] = static_cast<float>(exp(logdecay));
+    if (!OUT && tile == 0 && tid < 32) {
+        if (tid >= kTok) logdecay = 0.0;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) logdecay += __shfl_xor_sync(0xffffffffu, logdecay, o);
+        if (tid == 0) p.seg_decay[bh * p.split.pieces() + seg] = exp2_of(logdecay * 1.4426950408889634074);
+    }
 }
 
 // Turns what the pieces add into the states the segments start from, in token order; four
@@ -150,21 +168,28 @@ __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
     *at = s;
 }
 
-template <int N>
+template <int N, int NR, int PT>
 cudaError_t go(const SsmParams& p, cudaStream_t s)
 {
-    constexpr int NS = N / 16;
-    const int threads = p.P * NS < 128 ? p.P * NS : 128;
-    const int pt = threads / NS;
-    const size_t smem = sizeof(float) * (2 * kTok * N + kTok * pt + 2 * kTok);
-    const unsigned gx = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * (p.P / pt));
+    const unsigned gx = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * (p.P / PT));
     if (p.split.nseg > 1) {
-        k_ssm_scan<N, false><<<dim3(gx, p.split.pieces()), threads, smem, s>>>(p);
+        k_ssm_scan<N, NR, PT, false><<<dim3(gx, p.split.pieces()), PT * (N / NR), 0, s>>>(p);
         const cudaError_t e = launch_ssm_chain(p, s);
         if (e != cudaSuccess) return e;
     }
-    k_ssm_scan<N, true><<<dim3(gx, p.split.nseg), threads, smem, s>>>(p);
+    k_ssm_scan<N, NR, PT, true><<<dim3(gx, p.split.nseg), PT * (N / NR), 0, s>>>(p);
     return cudaGetLastError();
+}
+
+// 16 state values per thread, and as many channels as make 128 threads; small heads hold fewer values per thread
+// instead (64 threads at the least).
+template <int N>
+cudaError_t shape(const SsmParams& p, cudaStream_t s)
+{
+    if constexpr (N >= 128) return go<N, 16, 2048 / N>(p, s);
+    else if (p.P >= 64) return go<N, 16, 128 * 16 / N < 64 ? 128 * 16 / N : 64>(p, s);
+    else if (p.P == 32) return go<N, N == 16 ? 4 : N / 4, 32>(p, s);
+    else return go<N, N == 16 ? 4 : N / 8, 16>(p, s);
 }
 
 }  // namespace
@@ -207,11 +232,11 @@ SsmSplit ssm_split(int B, int T, int H, int G, int P)
 cudaError_t launch_ssm_plain(const SsmParams& p, cudaStream_t s)
 {
     switch (p.N) {
-        case 16: return go<16>(p, s);
-        case 32: return go<32>(p, s);
-        case 64: return go<64>(p, s);
-        case 128: return go<128>(p, s);
-        case 256: return go<256>(p, s);
+        case 16: return shape<16>(p, s);
+        case 32: return shape<32>(p, s);
+        case 64: return shape<64>(p, s);
+        case 128: return shape<128>(p, s);
+        case 256: return shape<256>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }
