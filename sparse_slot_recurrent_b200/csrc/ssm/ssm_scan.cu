@@ -6,7 +6,12 @@
 // registers (NR = 16, fewer for small heads, so that a block has 128 threads).  Blocks of kTok tokens of B, C, x and the
 // step sizes go through shared memory; while one is worked on, the next is on its way into registers.  Per token a
 // thread takes 3 NR multiply-adds and a log2(NS)-step lane sum.
+// k_ssm_tile, for heads of at least 64 x 32 values or so: a thread holds 8 state values of 4 channels, so that a token's
+// loads from shared memory (5 x 16 bytes) serve 96 multiply-adds, taken in pairs; the lane sum scatters 4 channels while it
+// adds, and y leaves through shared memory.  (k_ssm_scan moves four times the shared memory per value: 9.8 ms for
+// B4 T16384 H16 P128 N128 in fp32, against @TILE@ ms.)
 // Bound: fp32 issue (3 N P per token-head) and, with few heads, the latency of the token chain.
+#include "pairs.cuh"
 #include "ssm_common.cuh"
 
 namespace ramnet {
@@ -14,7 +19,20 @@ namespace {
 
 constexpr int kTok = 16;
 
-template <int N, int NR, int PT, bool OUT>
+// One input value's bits, and the value: kept apart, so that loads that are in flight wait for nothing.
+template <bool BF>
+__device__ __forceinline__ uint32_t bits_at(const void* p, int64_t i)
+{
+    if constexpr (BF) return reinterpret_cast<const uint16_t*>(p)[i];
+    else return reinterpret_cast<const uint32_t*>(p)[i];
+}
+template <bool BF>
+__device__ __forceinline__ float value_of(uint32_t bits)
+{
+    return __uint_as_float(BF ? bits << 16 : bits);
+}
+
+template <int N, int NR, int PT, bool BF, bool OUT>
 __global__ void __launch_bounds__(PT * (N / NR)) k_ssm_scan(SsmParams p)
 {
     constexpr int NS = N / NR, TH = PT * NS;  // lanes per channel, threads
@@ -46,20 +64,20 @@ __global__ void __launch_bounds__(PT * (N / NR)) k_ssm_scan(SsmParams p)
         S[k] = start ? start[static_cast<int64_t>(n) * p.P + ch] : 0.0f;
     }
     // the block of tokens from t0, into registers (tokens that are not there as zeros)
-    float vB[LB], vC[LB], vX[LX], vD = 0.0f;
+    uint32_t vB[LB], vC[LB], vX[LX], vD = 0;
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int k = 0; k < LB; ++k) {
             const int i = k * TH + tid, t = t0 + i / N, n = i % N;
-            vB[k] = t < r.last ? load_in(p.Bm, static_cast<size_t>(b * p.bs.b + t * p.bs.t + g * p.bs.h + n), p.in_bf16) : 0.0f;
-            if (OUT) vC[k] = t < r.last ? load_in(p.Cm, static_cast<size_t>(b * p.cs.b + t * p.cs.t + g * p.cs.h + n), p.in_bf16) : 0.0f;
+            vB[k] = t < r.last ? bits_at<BF>(p.Bm, b * p.bs.b + t * p.bs.t + g * p.bs.h + n) : 0u;
+            if (OUT) vC[k] = t < r.last ? bits_at<BF>(p.Cm, b * p.cs.b + t * p.cs.t + g * p.cs.h + n) : 0u;
         }
 #pragma unroll
         for (int k = 0; k < LX; ++k) {
             const int i = k * TH + tid, t = t0 + i / PT;
-            vX[k] = i < kTok * PT && t < r.last ? load_in(p.x, static_cast<size_t>(b * p.xs.b + t * p.xs.t + h * p.xs.h + tile * PT + i % PT), p.in_bf16) : 0.0f;
+            vX[k] = i < kTok * PT && t < r.last ? bits_at<BF>(p.x, b * p.xs.b + t * p.xs.t + h * p.xs.h + tile * PT + i % PT) : 0u;
         }
-        if (tid < kTok && t0 + tid < r.last) vD = load_in(p.dt, static_cast<size_t>(b * p.dts.b + (t0 + tid) * p.dts.t + h * p.dts.h), p.in_bf16);
+        if (tid < kTok && t0 + tid < r.last) vD = bits_at<BF>(p.dt, b * p.dts.b + (t0 + tid) * p.dts.t + h * p.dts.h);
     };
     double logdecay = 0.0;  // of this thread's tokens (the first kTok threads)
     if (r.first < r.last) fetch(r.first);
@@ -68,14 +86,14 @@ __global__ void __launch_bounds__(PT * (N / NR)) k_ssm_scan(SsmParams p)
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < LB; ++k) {
-            sB[k * TH + tid] = vB[k];
-            if (OUT) sC[k * TH + tid] = vC[k];
+            sB[k * TH + tid] = value_of<BF>(vB[k]);
+            if (OUT) sC[k * TH + tid] = value_of<BF>(vC[k]);
         }
 #pragma unroll
         for (int k = 0; k < LX; ++k)
-            if (k * TH + tid < kTok * PT) sX[k * TH + tid] = vX[k];
+            if (k * TH + tid < kTok * PT) sX[k * TH + tid] = value_of<BF>(vX[k]);
         if (tid < nt) {
-            const float d = step_size(vD, bias, p.softplus, p.dt_min, p.dt_max);
+            const float d = step_size(value_of<BF>(vD), bias, p.softplus, p.dt_min, p.dt_max);
             const double l = static_cast<double>(d) * A;
             sD[tid] = d;
             // rounded once from 64 bits: a bias of expf, a fraction of an ulp, would add up over
@@ -128,6 +146,171 @@ __global__ void __launch_bounds__(PT * (N / NR)) k_ssm_scan(SsmParams p)
     }
 }
 
+// Threads of k_ssm_tile: N/8 neighbouring lanes for 4 channels, PT channels per block.
+template <int N, int PT, bool BF, bool OUT>
+__global__ void __launch_bounds__(N / 8 * (PT / 4)) k_ssm_tile(SsmParams p)
+{
+    constexpr int kTok = N > 128 ? 8 : 16;  // (the next block's registers)
+    constexpr int NG = N / 8, TH = NG * (PT / 4);
+    constexpr int LB = kTok * N / TH, LX = kTok * PT / TH;
+    static_assert(NG <= 32 && LB * TH == kTok * N && LX * TH == kTok * PT, "shape");
+    __shared__ __align__(16) float sB[kTok * N], sC[OUT ? kTok * N : 4], sX[kTok * PT], sY[OUT ? kTok * PT : 4], sA[kTok], sD[kTok];
+    const int seg = blockIdx.y, tid = threadIdx.x;
+    const int ptiles = p.P / PT;
+    const int tile = static_cast<int>(blockIdx.x % ptiles);
+    const int64_t bh = blockIdx.x / ptiles;
+    const int h = static_cast<int>(bh % p.H);
+    const int64_t b = bh / p.H;
+    const int g = h / (p.H / p.G);
+    const SegRange r = seg_range(seq_len(p.lengths, static_cast<int>(b), p.T), seg, OUT ? p.split.seg_len : p.split.piece_len());
+    const int s = tid % NG, pl = tid / NG * 4;  // lane's place among the state values; its first channel
+    const int64_t np = static_cast<int64_t>(N) * p.P;
+    const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f, skip = p.D ? p.D[h] : 0.0f;
+
+    // values n = 4 (s + NG (k/2)) + 2 (k%2) and n + 1, for k < 4, of channels pl + q
+    F2 S[4][4];
+    auto at = [&](int k) { return 4 * (s + NG * (k >> 1)) + 2 * (k & 1); };
+    const float* start = nullptr;
+    if (OUT) {
+        if (p.split.nseg > 1) start = p.seg_state + (bh * p.split.slots() + seg * p.split.sub) * np;
+        else if (p.S_in) start = p.S_in + bh * np;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float4 lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f), hi = lo;
+        if (start) {
+            lo = *reinterpret_cast<const float4*>(start + static_cast<int64_t>(at(k)) * p.P + tile * PT + pl);
+            hi = *reinterpret_cast<const float4*>(start + static_cast<int64_t>(at(k) + 1) * p.P + tile * PT + pl);
+        }
+        S[k][0] = f2(lo.x, hi.x), S[k][1] = f2(lo.y, hi.y), S[k][2] = f2(lo.z, hi.z), S[k][3] = f2(lo.w, hi.w);
+    }
+    // the block of tokens from t0, into registers (tokens that are not there as zeros)
+    uint32_t vB[LB], vC[LB], vX[LX], vD = 0;
+    auto fetch = [&](int t0) {
+#pragma unroll
+        for (int k = 0; k < LB; ++k) {
+            const int i = k * TH + tid, t = t0 + i / N, n = i % N;
+            vB[k] = t < r.last ? bits_at<BF>(p.Bm, b * p.bs.b + t * p.bs.t + g * p.bs.h + n) : 0u;
+            if (OUT) vC[k] = t < r.last ? bits_at<BF>(p.Cm, b * p.cs.b + t * p.cs.t + g * p.cs.h + n) : 0u;
+        }
+#pragma unroll
+        for (int k = 0; k < LX; ++k) {
+            const int i = k * TH + tid, t = t0 + i / PT;
+            vX[k] = t < r.last ? bits_at<BF>(p.x, b * p.xs.b + t * p.xs.t + h * p.xs.h + tile * PT + i % PT) : 0u;
+        }
+        if (tid < kTok && t0 + tid < r.last) vD = bits_at<BF>(p.dt, b * p.dts.b + (t0 + tid) * p.dts.t + h * p.dts.h);
+    };
+    auto leave = [&](int t0, int nt) {  // y of the block of nt tokens from t0
+#pragma unroll
+        for (int k = 0; k < LX; ++k) {
+            const int i = k * TH + tid;
+            if (i / PT < nt)
+                store_out(p.y, static_cast<size_t>(((b * p.T + t0 + i / PT) * p.H + h) * p.P + tile * PT + i % PT), sY[i], p.out_bf16);
+        }
+    };
+    double logdecay = 0.0;  // of this thread's tokens (the first kTok threads)
+    if (r.first < r.last) fetch(r.first);
+    for (int t0 = r.first; t0 < r.last; t0 += kTok) {
+        const int nt = min(kTok, r.last - t0);
+        __syncthreads();
+        if (OUT && t0 > r.first) leave(t0 - kTok, kTok);
+#pragma unroll
+        for (int k = 0; k < LB; ++k) {
+            sB[k * TH + tid] = value_of<BF>(vB[k]);
+            if (OUT) sC[k * TH + tid] = value_of<BF>(vC[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < LX; ++k) sX[k * TH + tid] = value_of<BF>(vX[k]);
+        if (tid < nt) {
+            const float d = step_size(value_of<BF>(vD), bias, p.softplus, p.dt_min, p.dt_max);
+            const double l = static_cast<double>(d) * A;
+            sD[tid] = d;
+            sA[tid] = exp2_of(l * 1.4426950408889634074);  // rounded once from 64 bits, as in k_ssm_scan
+            logdecay += l;
+        }
+        __syncthreads();
+        if (t0 + kTok < r.last) fetch(t0 + kTok);
+#pragma unroll 2
+        for (int t = 0; t < nt; ++t) {
+            const float av = sA[t], dv = sD[t];
+            const float4 xv = *reinterpret_cast<const float4*>(sX + t * PT + pl);
+            const F2 a = f2(av, av);
+            const F2 u[4] = {f2(dv * xv.x, dv * xv.x), f2(dv * xv.y, dv * xv.y), f2(dv * xv.z, dv * xv.z), f2(dv * xv.w, dv * xv.w)};
+            F2 y[4] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f), f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+#pragma unroll
+            for (int k2 = 0; k2 < 2; ++k2) {
+                const float4 bv = *reinterpret_cast<const float4*>(sB + t * N + 4 * (s + NG * k2));
+                const F2 bb[2] = {f2(bv.x, bv.y), f2(bv.z, bv.w)};
+                F2 cc[2];
+                if (OUT) {
+                    const float4 cv = *reinterpret_cast<const float4*>(sC + t * N + 4 * (s + NG * k2));
+                    cc[0] = f2(cv.x, cv.y), cc[1] = f2(cv.z, cv.w);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        F2& v = S[2 * k2 + j][q];
+                        v = fma2(bb[j], u[q], mul2(a, v));
+                        if (OUT) y[q] = fma2(cc[j], v, y[q]);
+                    }
+            }
+            if (OUT) {
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float e, f;
+                    un(y[q], e, f);
+                    v[q] = e + f;
+                }
+                // sums over the lanes of these channels: halves of the channels are handed over first, then whole lanes
+                const bool up = s & 1, up2 = s & 2;
+                float k0 = up ? v[2] : v[0], k1 = up ? v[3] : v[1];
+                k0 += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 1);
+                k1 += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 1);
+                int ch = up ? 2 : 0;
+                if constexpr (NG >= 4) {
+                    float k = up2 ? k1 : k0;
+                    k += __shfl_xor_sync(0xffffffffu, up2 ? k0 : k1, 2);
+                    ch += up2 ? 1 : 0;
+#pragma unroll
+                    for (int o = 4; o < NG; o <<= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+                    if (s < 4) sY[t * PT + pl + ch] = fmaf(skip, sX[t * PT + pl + ch], k);
+                } else {
+                    sY[t * PT + pl + ch] = fmaf(skip, sX[t * PT + pl + ch], k0);
+                    sY[t * PT + pl + ch + 1] = fmaf(skip, sX[t * PT + pl + ch + 1], k1);
+                }
+            }
+        }
+    }
+    if (OUT && r.first < r.last) {
+        __syncthreads();
+        const int done = (r.last - r.first - 1) / kTok * kTok;
+        leave(r.first + done, r.last - r.first - done);
+    }
+    float* end = nullptr;
+    if (!OUT) end = p.seg_state + (bh * p.split.slots() + seg) * np;
+    else if (seg == p.split.nseg - 1) end = p.S_out + bh * np;
+    if (end) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float4 lo, hi;
+            un(S[k][0], lo.x, hi.x);
+            un(S[k][1], lo.y, hi.y);
+            un(S[k][2], lo.z, hi.z);
+            un(S[k][3], lo.w, hi.w);
+            *reinterpret_cast<float4*>(end + static_cast<int64_t>(at(k)) * p.P + tile * PT + pl) = lo;
+            *reinterpret_cast<float4*>(end + static_cast<int64_t>(at(k) + 1) * p.P + tile * PT + pl) = hi;
+        }
+    }
+    if (!OUT && tile == 0 && tid < 32) {
+        if (tid >= kTok) logdecay = 0.0;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) logdecay += __shfl_xor_sync(0xffffffffu, logdecay, o);
+        if (tid == 0) p.seg_decay[bh * p.split.pieces() + seg] = exp2_of(logdecay * 1.4426950408889634074);
+    }
+}
+
 // Turns what the pieces add into the states the segments start from, in token order; four
 // neighbouring state values per thread, one (sequence, head) per blockIdx.y.  With chunk totals the
 // pieces' decays come from those, else from seg_decay.
@@ -168,28 +351,47 @@ __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
     *at = s;
 }
 
-template <int N, int NR, int PT>
-cudaError_t go(const SsmParams& p, cudaStream_t s)
+template <class K1, class K2>
+cudaError_t launches(const SsmParams& p, K1 pieces, K2 outputs, int pt, int threads, cudaStream_t s)
 {
-    const unsigned gx = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * (p.P / PT));
+    const unsigned gx = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * (p.P / pt));
     if (p.split.nseg > 1) {
-        k_ssm_scan<N, NR, PT, false><<<dim3(gx, p.split.pieces()), PT * (N / NR), 0, s>>>(p);
+        pieces<<<dim3(gx, p.split.pieces()), threads, 0, s>>>(p);
         const cudaError_t e = launch_ssm_chain(p, s);
         if (e != cudaSuccess) return e;
     }
-    k_ssm_scan<N, NR, PT, true><<<dim3(gx, p.split.nseg), PT * (N / NR), 0, s>>>(p);
+    outputs<<<dim3(gx, p.split.nseg), threads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
-// 16 state values per thread, and as many channels as make 128 threads; small heads hold fewer values per thread
-// instead (64 threads at the least).
+template <int N, int NR, int PT>
+cudaError_t small(const SsmParams& p, cudaStream_t s)
+{
+    return p.in_bf16 ? launches(p, k_ssm_scan<N, NR, PT, true, false>, k_ssm_scan<N, NR, PT, true, true>, PT, PT * (N / NR), s)
+                     : launches(p, k_ssm_scan<N, NR, PT, false, false>, k_ssm_scan<N, NR, PT, false, true>, PT, PT * (N / NR), s);
+}
+
+template <int N, int PT>
+cudaError_t tiled(const SsmParams& p, cudaStream_t s)
+{
+    return p.in_bf16 ? launches(p, k_ssm_tile<N, PT, true, false>, k_ssm_tile<N, PT, true, true>, PT, N / 8 * (PT / 4), s)
+                     : launches(p, k_ssm_tile<N, PT, false, false>, k_ssm_tile<N, PT, false, true>, PT, N / 8 * (PT / 4), s);
+}
+
+// The tiled form where a head makes a block of at least 64 threads of it (128 at most, over 4096/N channels); else 4 to 16
+// values per thread so that the head still makes 64 or 128.
 template <int N>
 cudaError_t shape(const SsmParams& p, cudaStream_t s)
 {
-    if constexpr (N >= 128) return go<N, 16, 2048 / N>(p, s);
-    else if (p.P >= 64) return go<N, 16, 128 * 16 / N < 64 ? 128 * 16 / N : 64>(p, s);
-    else if (p.P == 32) return go<N, N == 16 ? 4 : N / 4, 32>(p, s);
-    else return go<N, N == 16 ? 4 : N / 8, 16>(p, s);
+    constexpr int most = 4096 / N;
+    if (p.P >= most) return tiled<N, most>(p, s);
+    if (2 * p.P >= most) return tiled<N, most / 2>(p, s);
+    if constexpr (N == 64) return small<N, 8, 16>(p, s);
+    if constexpr (N < 64) {
+        if (p.P >= 64) return small<N, 16, 64>(p, s);
+        return p.P == 32 ? small<N, N / 4, 32>(p, s) : small<N, 4, 16>(p, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
