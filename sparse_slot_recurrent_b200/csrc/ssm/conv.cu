@@ -4,7 +4,7 @@
 // with the W-1 inputs before the first token taken from a carried state.  Sums in fp32.
 //
 // Bound: HBM, one read of x and one write of y (2 W flops per element).  A thread owns V
-// neighbouring channels (16 bytes where addresses allow) over a run of tokens and slides a
+// neighbouring channels (16 bytes, or what addresses allow) over a run of tokens and slides a
 // window of W-1 inputs in registers, so each input is read once but for W-1 rows per run (which
 // the run before has just brought into L2).  Rows come through a ring in shared memory that
 // only its own thread fills and reads, up to fourteen in flight.  For 4 x 16384 x 2304 bf16 channels: 273 us with one
@@ -20,9 +20,11 @@ constexpr int kRunShort = 16, kRunLong = 64;  // tokens per thread
 constexpr int kDepth = 8;   // steps of two rows in a thread's ring: seven in flight, one in use
 static_assert(kRunShort % 8 == 0 && kRunLong % 8 == 0, "whole steps");
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src)
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 template <int W, int V, bool IB, bool OB>
@@ -41,7 +43,9 @@ __global__ void __launch_bounds__(128, V > 1 ? 4 : 1) k_conv(ConvParams p, int n
     if (t0 >= len && t0 > 0) return;
     const int t1 = min(t0 + run_len, len);
     constexpr int H = (V + 1) / 2;            // pairs of channels
-    constexpr int kBatch = V > 1 ? 2 : 8;     // rows per step (single values: in registers)
+    constexpr int kBytes = Raw<IB, V>::kBytes;
+    constexpr bool kRing = kBytes >= 4;       // what copies itself; a lone bf16 value comes through registers
+    constexpr int kBatch = kRing ? 2 : 8;     // rows per step
 
     Val<V> wt[W][H], bias[H], win[W + kBatch - 1][H];
     {
@@ -78,9 +82,9 @@ __global__ void __launch_bounds__(128, V > 1 ? 4 : 1) k_conv(ConvParams p, int n
         else old[k].clear();
         old[k].widen(win[k]);
     }
-    // each thread's own ring of rows in shared memory, or (single values) one step in registers
-    __shared__ uint4 ring[V > 1 ? kDepth * kBatch * 128 : 1];
-    const uint32_t mine = smem_addr(ring + (V > 1 ? threadIdx.x : 0));
+    // each thread's own ring of rows in shared memory, or one step in registers
+    __shared__ __align__(16) unsigned char ring[kRing ? kDepth * kBatch * 128 * kBytes : 16];
+    const uint32_t mine = smem_addr(ring) + threadIdx.x * kBytes;
     Raw<IB, V> next[kBatch];
     const unsigned char* src = reinterpret_cast<const unsigned char*>(p.x) + (xb + static_cast<int64_t>(t0) * p.st) * (IB ? 2 : 4);
     const int64_t stride = p.st * (IB ? 2 : 4);
@@ -88,26 +92,23 @@ __global__ void __launch_bounds__(128, V > 1 ? 4 : 1) k_conv(ConvParams p, int n
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
             if (t + i < t1) {
-                if constexpr (V > 1) copy16(mine + ((((t - t0) & (kDepth * kBatch - 1)) + i) << 11), src + (t - t0 + i) * stride);
+                if constexpr (kRing) copy_async<kBytes>(mine + (((t - t0) & (kDepth * kBatch - 1)) + i) * (128 * kBytes), src + (t - t0 + i) * stride);
                 else next[i].load(p.x, xb + static_cast<int64_t>(t + i) * p.st);
             }
-        if constexpr (V > 1) asm volatile("cp.async.commit_group;" ::: "memory");
+        if constexpr (kRing) asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int d = 0; d < (V > 1 ? kDepth - 1 : 1); ++d) fetch(t0 + d * kBatch);
+    for (int d = 0; d < (kRing ? kDepth - 1 : 1); ++d) fetch(t0 + d * kBatch);
 #pragma unroll 1
     for (int t = t0; t < t1; t += kBatch) {
-        if constexpr (V > 1) {
+        if constexpr (kRing) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const uint4 v = ring[(((t - t0) & (kDepth * kBatch - 1)) + i) * 128 + threadIdx.x];
-                next[i].set(v);
-            }
+            for (int i = 0; i < kBatch; ++i) next[i].take(ring + (((t - t0) & (kDepth * kBatch - 1)) + i) * (128 * kBytes) + threadIdx.x * kBytes);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) next[i].widen(win[W - 1 + i]);
-        fetch(t + (V > 1 ? (kDepth - 1) * kBatch : kBatch));
+        fetch(t + (kRing ? (kDepth - 1) * kBatch : kBatch));
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             float y[V];
@@ -178,8 +179,6 @@ __global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p, int ncv, in
     for (int k = 0; k < W - 1; ++k) in[k + 1].store(p.state, sbase + static_cast<int64_t>(k) * p.C);
 }
 
-bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 template <int W, int V, bool IB, bool OB>
 cudaError_t go(const ConvParams& p, cudaStream_t s)
 {
@@ -201,46 +200,39 @@ cudaError_t go(const ConvStepParams& p, cudaStream_t s)
     return cudaGetLastError();
 }
 
-template <int W, bool IB, class P>
-cudaError_t pick_v(const P& p, bool vec, cudaStream_t s)
+template <int W, int V, bool IB, class P>
+cudaError_t pick_out(const P& p, cudaStream_t s)
 {
-    constexpr int V = IB ? 8 : 4;
-    if (vec) return p.out_bf16 ? go<W, V, IB, true>(p, s) : go<W, V, IB, false>(p, s);
-    return p.out_bf16 ? go<W, 1, IB, true>(p, s) : go<W, 1, IB, false>(p, s);
+    return p.out_bf16 ? go<W, V, IB, true>(p, s) : go<W, V, IB, false>(p, s);
 }
 
 template <int W, class P>
-cudaError_t pick_in(const P& p, bool vec, cudaStream_t s)
+cudaError_t pick_v(const P& p, int v, cudaStream_t s)
 {
-    return p.in_bf16 ? pick_v<W, true>(p, vec, s) : pick_v<W, false>(p, vec, s);
+    if (p.in_bf16) {
+        if (v == 8) return pick_out<W, 8, true>(p, s);
+        return v >= 2 ? pick_out<W, 2, true>(p, s) : pick_out<W, 1, true>(p, s);
+    }
+    if (v == 4) return pick_out<W, 4, false>(p, s);
+    return v == 2 ? pick_out<W, 2, false>(p, s) : pick_out<W, 1, false>(p, s);
 }
 
 template <class P>
-cudaError_t pick_w(const P& p, bool vec, cudaStream_t s)
+cudaError_t pick_w(const P& p, int v, cudaStream_t s)
 {
     switch (p.W) {
-        case 2: return pick_in<2>(p, vec, s);
-        case 3: return pick_in<3>(p, vec, s);
-        case 4: return pick_in<4>(p, vec, s);
+        case 2: return pick_v<2>(p, v, s);
+        case 3: return pick_v<3>(p, v, s);
+        case 4: return pick_v<4>(p, v, s);
         default: return cudaErrorInvalidValue;
     }
 }
 
 }  // namespace
 
-cudaError_t launch_conv(const ConvParams& p, cudaStream_t s)
-{
-    // 16-byte accesses need every row of x, y and the states to start on a 16-byte boundary
-    const int v = p.in_bf16 ? 8 : 4;
-    const bool vec = p.C % v == 0 && p.sb % v == 0 && p.st % v == 0 && al(p.x, 16);
-    return pick_w(p, vec, s);
-}
+// (y and the states start on 16 bytes, and their rows follow from C)
+cudaError_t launch_conv(const ConvParams& p, cudaStream_t s) { return pick_w(p, widest(p.in_bf16, {p.C, p.sb, p.st}, {p.x}), s); }
 
-cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t s)
-{
-    const int v = p.in_bf16 ? 8 : 4;
-    const bool vec = p.C % v == 0 && p.sb % v == 0 && al(p.x, 16);
-    return pick_w(p, vec, s);
-}
+cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t s) { return pick_w(p, widest(p.in_bf16, {p.C, p.sb}, {p.x}), s); }
 
 }  // namespace ramnet

@@ -6,8 +6,8 @@
 //
 // Bound: HBM, x and z read once and y written once.  k_norm_warp: one warp per group of one row,
 // with all of the group's loads in flight before the first is used and no barrier (groups up to
-// 256 16-byte vectors: 2048 bf16 or 1024 fp32 channels).  k_norm_block: one block per group, for longer groups and for rows
-// that do not start on 16 bytes; what it does not keep in registers it reads again, from L2.
+// 256 vectors: 2048 bf16 or 1024 fp32 channels at 16 bytes).  k_norm_block: one block per group, for longer groups; what it
+// does not keep in registers it reads again, from L2.  Vectors are as wide as rows and addresses allow.
 // (One block per row for all: 229 us for 65536 x 2048 bf16 rows, the block's barrier and its few
 // bytes in flight.)
 #include "rows.cuh"
@@ -36,18 +36,19 @@ __global__ void __launch_bounds__(128, 4) k_norm_warp(NormParams p)
         }
     }
     const bool pre = PRE && p.z;
-    F2 u[NV][V / 2], sum2 = f2(0.0f, 0.0f);
+    constexpr int H = (V + 1) / 2;
+    Val<V> u[NV][H], sum2 = val<V>(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int h = 0; h < V / 2; ++h) {
+        for (int h = 0; h < H; ++h) {
             u[k][h] = x[k].pair(h);
             if (pre) u[k][h] = mul2(u[k][h], silu2<OB>(z[k].pair(h)));
             sum2 = fma2(u[k][h], u[k][h], sum2);
         }
-    float sum, other;
-    un(sum2, sum, other);
-    sum += other;
+    float both[V > 1 ? V : 1] = {};
+    put<V>(sum2, 0, both);
+    float sum = both[0] + (V > 1 ? both[V > 1 ? 1 : 0] : 0.0f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     const float inv = 1.0f / sqrtf(sum / static_cast<float>(width) + p.eps);
@@ -57,14 +58,15 @@ __global__ void __launch_bounds__(128, 4) k_norm_warp(NormParams p)
         if (i < nv) {
             float y[V];
 #pragma unroll
-            for (int h = 0; h < V / 2; ++h) {
-                F2 v = mul2(u[k][h], f2(inv, inv));
+            for (int h = 0; h < H; ++h) {
+                Val<V> v = mul2(u[k][h], val<V>(inv, inv));
                 if (p.w) {
-                    const float2 w = *reinterpret_cast<const float2*>(p.w + d + 2 * h);
-                    v = mul2(v, f2(w.x, w.y));
+                    Raw<false, V == 1 ? 1 : 2> w;
+                    w.load(p.w, d + 2 * h);
+                    v = mul2(v, w.pair(0));
                 }
                 if (!PRE) v = mul2(v, silu2<OB>(z[k].pair(h)));
-                un(v, y[2 * h], y[2 * h + 1]);
+                put<V>(v, h, y);
             }
             store_vec<OB, V>(p.y, row * p.D + d, y);
         }
@@ -148,8 +150,6 @@ __global__ void __launch_bounds__(kThreads) k_norm_block(NormParams p)
     }
 }
 
-bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 template <int V, int NV, bool IB>
 cudaError_t block(const NormParams& p, cudaStream_t s)
 {
@@ -170,24 +170,29 @@ cudaError_t warp(const NormParams& p, cudaStream_t s)
 }
 
 template <int V, bool IB>
-cudaError_t pick(const NormParams& p, int nv, cudaStream_t s)
+cudaError_t pick(const NormParams& p, cudaStream_t s)
 {
-    if (nv <= 32) return warp<V, 1, IB>(p, s);
+    const int nv = p.D / p.groups / V;
+    if constexpr (Raw<IB, V>::kBytes == 16) {
+        if (nv <= 32) return warp<V, 1, IB>(p, s);
+        if (nv > 64 && nv <= 128) return warp<V, 4, IB>(p, s);
+    }
     if (nv <= 64) return warp<V, 2, IB>(p, s);
-    if (nv <= 128) return warp<V, 4, IB>(p, s);
     if (nv <= 256) return warp<V, 8, IB>(p, s);
-    return block<V, 2, IB>(p, s);
+    return block<V, V == 8 ? 2 : 4, IB>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_gate(const NormParams& p, cudaStream_t s)
 {
-    const int v = p.in_bf16 ? 8 : 4;
-    const int width = p.D / p.groups;
-    const bool vec = width % v == 0 && p.sx % v == 0 && al(p.x, 16) && (!p.z || (p.sz % v == 0 && al(p.z, 16)));
-    if (p.in_bf16) return vec ? pick<8, true>(p, width / 8, s) : block<1, 4, true>(p, s);
-    return vec ? pick<4, false>(p, width / 4, s) : block<1, 4, false>(p, s);
+    const int v = widest(p.in_bf16, {p.D / p.groups, p.sx, p.z ? p.sz : 0}, {p.x, p.z});
+    if (p.in_bf16) {
+        if (v == 8) return pick<8, true>(p, s);
+        return v >= 2 ? pick<2, true>(p, s) : pick<1, true>(p, s);
+    }
+    if (v == 4) return pick<4, false>(p, s);
+    return v == 2 ? pick<2, false>(p, s) : pick<1, false>(p, s);
 }
 
 }  // namespace ramnet

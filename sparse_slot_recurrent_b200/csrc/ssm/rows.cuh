@@ -2,6 +2,7 @@
 // neighbouring values (16 bytes, or one value where addresses do not allow that), SiLU.
 #pragma once
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "../common.cuh"
@@ -29,35 +30,35 @@ __device__ __forceinline__ void put(Val<V> p, int h, float (&y)[V])
     else un(p, y[2 * h], y[2 * h + 1]);
 }
 
-// V values as they lie in memory, bf16 (BF) or fp32; V is 1 or fills 16 bytes.
+// V values as they lie in memory, bf16 (BF) or fp32: one value, or 4, 8 or 16 bytes.
 template <bool BF, int V>
 struct Raw {
-    static constexpr int kWords = V == 1 ? 1 : 4;
+    static constexpr int kBytes = V * (BF ? 2 : 4);
+    static constexpr int kWords = kBytes >= 4 ? kBytes / 4 : 1;
+    static_assert(kBytes <= 16 && (V & (V - 1)) == 0, "one access");
     uint32_t r[kWords];
 
-    __device__ __forceinline__ void load(const void* base, int64_t i)
+    __device__ __forceinline__ void take(const void* at)
     {
-        if constexpr (V == 1) {
-            if constexpr (BF) r[0] = reinterpret_cast<const uint16_t*>(base)[i];
-            else r[0] = reinterpret_cast<const uint32_t*>(base)[i];
-        } else {
-            const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(base) + i * (16 / V));
+        if constexpr (kBytes == 2) r[0] = *reinterpret_cast<const uint16_t*>(at);
+        if constexpr (kBytes == 4) r[0] = *reinterpret_cast<const uint32_t*>(at);
+        if constexpr (kBytes == 8) {
+            const uint2 v = *reinterpret_cast<const uint2*>(at);
+            r[0] = v.x, r[1] = v.y;
+        }
+        if constexpr (kBytes == 16) {
+            const uint4 v = *reinterpret_cast<const uint4*>(at);
             r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
         }
     }
+    __device__ __forceinline__ void load(const void* base, int64_t i) { take(reinterpret_cast<const unsigned char*>(base) + i * (BF ? 2 : 4)); }
     __device__ __forceinline__ void store(void* base, int64_t i) const
     {
-        if constexpr (V == 1) {
-            if constexpr (BF) reinterpret_cast<uint16_t*>(base)[i] = static_cast<uint16_t>(r[0]);
-            else reinterpret_cast<uint32_t*>(base)[i] = r[0];
-        } else {
-            *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(base) + i * (16 / V)) = make_uint4(r[0], r[1], r[2], r[3]);
-        }
-    }
-    __device__ __forceinline__ void set(uint4 v)
-    {
-        static_assert(V > 1, "16 bytes");
-        r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+        unsigned char* at = reinterpret_cast<unsigned char*>(base) + i * (BF ? 2 : 4);
+        if constexpr (kBytes == 2) *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(r[0]);
+        if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(at) = r[0];
+        if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(at) = make_uint2(r[0], r[1]);
+        if constexpr (kBytes == 16) *reinterpret_cast<uint4*>(at) = make_uint4(r[0], r[1], r[2], r[3]);
     }
     __device__ __forceinline__ void clear()
     {
@@ -77,18 +78,28 @@ struct Raw {
     }
 };
 
+// The widest vector, up to 16 bytes, that divides every number in `at` (element strides, lengths) and the addresses.
+inline int widest(bool bf16, std::initializer_list<int64_t> at, std::initializer_list<const void*> addresses)
+{
+    const int es = bf16 ? 2 : 4;
+    int v = 16 / es;
+    for (const int64_t n : at)
+        while (n % v != 0) v /= 2;
+    for (const void* p : addresses)
+        while (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(v * es) != 0) v /= 2;
+    return v;
+}
+
 template <bool BF, int V>
 __device__ __forceinline__ void store_vec(void* base, int64_t i, const float (&v)[V])
 {
     if constexpr (V == 1) {
         store_out(base, static_cast<size_t>(i), v[0], BF);
     } else if constexpr (BF) {
-        uint32_t u[V / 2];
+        Raw<true, V> u;
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) u[j] = pack_rn(f2(v[2 * j], v[2 * j + 1]));
-        __nv_bfloat16* p = reinterpret_cast<__nv_bfloat16*>(base) + i;
-        if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-        else *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+        for (int j = 0; j < V / 2; ++j) u.r[j] = pack_rn(f2(v[2 * j], v[2 * j + 1]));
+        u.store(base, i);
     } else {
         store_row_g<V>(reinterpret_cast<float*>(base) + i, v);
     }

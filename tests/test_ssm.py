@@ -229,7 +229,7 @@ def test_step_matches_plain_form(shape, dtype, out):
     _near(S, wS, E + 1e-30)
 
 
-CONV = [(1, 1, 1, 2), (1, 2, 8, 4), (2, 3, 16, 4), (3, 33, 24, 3), (2, 65, 17, 4), (2, 130, 520, 2), (1, 31, 7, 3)]
+CONV = [(1, 1, 1, 2), (2, 70, 6, 3), (1, 40, 12, 4), (1, 2, 8, 4), (2, 3, 16, 4), (3, 33, 24, 3), (2, 65, 17, 4), (2, 130, 520, 2), (1, 31, 7, 3)]
 
 
 def _conv_tol(wy, ya, W, silu, out):
@@ -288,7 +288,7 @@ def test_conv_ragged_in_place_and_single_tokens(dtype):
 
 
 NORM = [(1, 1, 1), (3, 8, 1), (5, 24, 3), (2, 2048, 1), (7, 1536, 2), (2, 17, 1), (2, 9000, 1), (1, 20000, 1), (3, 18000, 2),
-        (300, 64, 4), (1000, 100, 1)]
+        (300, 64, 4), (1000, 100, 1), (3, 1918, 1), (2, 348, 4), (2, 700, 2), (1, 3001, 1), (2, 6784, 4)]
 
 
 @pytest.mark.parametrize("shape", NORM, ids=str)
@@ -301,7 +301,7 @@ def test_norm_gate_matches_plain_form(shape, first, dtype, out):
     z = (3 * torch.randn((R, 2 * D + 1), generator=g)).to(dtype).cuda()[:, 1:D + 1]
     w = torch.randn((D,), generator=g).cuda()
     x[0] = 0  # a row of nothing: eps alone
-    for zz, ww in ((z, w), (z.contiguous(), None), (None, w)):
+    for zz, ww in ((z, w), (z.contiguous(), None), (None, w)):  # (the first on odd elements: single values)
         y = ramnet.norm_gate(x, z=zz, w=ww, groups=groups, eps=1e-5, gate_first=first, out_dtype=out)
         want = plain.norm_gate(x, zz, ww, groups, 1e-5, first)
         # a sum of squares off by (adds) u is half that in its root: at most D/groups/256 adds per thread and 13 more,
