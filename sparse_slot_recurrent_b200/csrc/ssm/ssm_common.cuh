@@ -27,12 +27,13 @@ cudaError_t launch_dependent(void (*kern)(Args...), dim3 grid, unsigned threads,
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// Step size of one token and head: softplus(dt + bias) (or dt + bias), clamped.
+// Step size of one token and head: softplus(dt + bias) (or dt + bias), clamped; what is no number stays none (fminf and
+// fmaxf alone would make a limit of it).
 __device__ __forceinline__ float step_size(float dt, float bias, int softplus, float lo, float hi)
 {
     float v = dt + bias;
     if (softplus) v = fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v)));
-    return fminf(fmaxf(v, lo), hi);
+    return v != v ? v : fminf(fmaxf(v, lo), hi);
 }
 
 // Tokens [first, last) of segment `seg` of a sequence of `len` tokens.
@@ -52,6 +53,7 @@ __device__ __forceinline__ SegRange seg_range(int len, int seg, int seg_len)
 // chunks that a slowly decaying state remembers.  Taylor series of 2^f, |f| <= 1/2, in 64 bits (error below 1e-11).
 __device__ __forceinline__ float exp2_of(double x)
 {
+    if (x != x) return static_cast<float>(x);
     x = fmin(fmax(x, -160.0), 160.0);
     const double n = rint(x), f = (x - n) * 0.69314718055994530942;
     double r = 1.0 / 362880;

@@ -229,6 +229,25 @@ def test_step_matches_plain_form(shape, dtype, out):
     _near(S, wS, E + 1e-30)
 
 
+@pytest.mark.parametrize("softplus", [True, False], ids=["softplus", "plain"])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_a_step_size_that_is_no_number_shows(dtype, softplus):
+    B, T, H, N, P = 2, 100, 3, 64, 64
+    cfg = ramnet.SsmConfig(H=H, G=1, N=N, P=P, dt_softplus=softplus)
+    L = _layer(B, T, H, 1, N, P, dtype)
+    clean = ramnet.ssm_forward(cfg, **L)
+    L["dt"][1, 70, 2] = float("nan")
+    y, S = ramnet.ssm_forward(cfg, **L)
+    assert bool(torch.isnan(y[1, 70:, 2]).all()) and bool(torch.isnan(S[1, 2]).all())
+    for b, h in ((0, 0), (0, 2), (1, 0), (1, 1)):
+        assert torch.equal(y[b, :, h], clean[0][b, :, h]) and torch.equal(S[b, h], clean[1][b, h])
+    assert torch.equal(y[1, :64, 2], clean[0][1, :64, 2])
+    S = torch.zeros((B, H, N, P), device="cuda")
+    y = ramnet.ssm_step(cfg, **{k: (v[:, 70] if v.dim() > 1 else v) for k, v in L.items()}, S=S)
+    assert bool(torch.isnan(y[1, 2]).all()) and bool(torch.isnan(S[1, 2]).all())
+    assert bool(torch.isfinite(S[0]).all()) and bool(torch.isfinite(S[1, :2]).all())
+
+
 CONV = [(1, 1, 1, 2), (2, 70, 6, 3), (1, 40, 12, 4), (1, 2, 8, 4), (2, 3, 16, 4), (3, 33, 24, 3), (2, 65, 17, 4), (2, 130, 520, 2), (1, 31, 7, 3)]
 
 
