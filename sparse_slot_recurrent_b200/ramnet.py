@@ -466,6 +466,9 @@ def ssm_forward(cfg: SsmConfig, x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=
     pout = _dense_ptr(S_out, "S_out", state, torch.float32, dev)
     if workspace is None:
         workspace = torch.empty(ssm_workspace_bytes(cfg, B, T), dtype=torch.uint8, device=x.device)
+        if stream is not None:  # it is given back when this call returns, and the work may still be waiting
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                    torch.cuda.ExternalStream(int(stream), device=x.device))
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous and on the device of x")
     _launch(dev, stream, load().ramnet_ssm_forward, cfg._ref, B, T, code, px, _strides_of(*x.stride()[:3]), pdt,

@@ -375,6 +375,31 @@ def test_layer_prompt_then_tokens_equals_one_prompt(dtype):
     assert torch.equal(cs, cs_all)
 
 
+def test_two_calls_at_once_on_streams_of_their_own():
+    """Two prompts on two streams, without workspaces of the caller's, interleaved with each other and with
+    allocations on the current stream; and a norm and a convolution on a stream that is passed in."""
+    B, T, H, G, N, P = 2, 700, 4, 2, 64, 64
+    cfg = ramnet.SsmConfig(H=H, G=G, N=N, P=P)
+    Ls = [_layer(B, T, H, G, N, P, BF, seed=s) for s in (1, 2)]
+    refs = [ramnet.ssm_forward(cfg, **L) for L in Ls]
+    flat = Ls[0]["x"].flatten(2).contiguous()
+    w = torch.ones((H * P, 4), device="cuda")
+    cref, nref = ramnet.conv_forward(flat, w), ramnet.norm_gate(flat.flatten(0, 1))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Ls]
+    outs = []
+    for rep in range(4):
+        for L, s in zip(Ls, streams):
+            outs.append(ramnet.ssm_forward(cfg, **L, stream=s))
+            torch.full((1 << 20,), float("nan"), device="cuda")
+    outs += [ramnet.ssm_forward(cfg, **L, stream=torch.cuda.current_stream().cuda_stream) for L in Ls]  # a raw handle
+    c, n = ramnet.conv_forward(flat, w, stream=streams[0]), ramnet.norm_gate(flat.flatten(0, 1), stream=streams[1])
+    torch.cuda.synchronize()
+    for i, (y, S) in enumerate(outs):
+        assert torch.equal(y, refs[i % 2][0]) and torch.equal(S, refs[i % 2][1])
+    assert torch.equal(c[0], cref[0]) and torch.equal(c[1], cref[1]) and torch.equal(n, nref)
+
+
 def test_other_stream_and_offsets_past_32_bits():
     """A call on a stream of its own, and operands whose last sequence starts beyond 2^31 elements."""
     H, G, N, P, T = 2, 1, 16, 16, 5
