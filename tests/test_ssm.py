@@ -248,6 +248,21 @@ def test_a_step_size_that_is_no_number_shows(dtype, softplus):
     assert bool(torch.isfinite(S[0]).all()) and bool(torch.isfinite(S[1, :2]).all())
 
 
+def test_thousands_of_single_tokens_keep_their_precision():
+    """A slowly decaying state stepped token by token: a bias of the decay's exponential would add up."""
+    T, H, N, P = 3000, 2, 16, 32
+    cfg = ramnet.SsmConfig(H=H, G=1, N=N, P=P)
+    L = _layer(1, T, H, 1, N, P, F32)
+    L["A"] = torch.tensor([-0.01, -0.3], device="cuda")
+    S = torch.zeros((1, H, N, P), device="cuda")
+    for t in range(T):
+        y = ramnet.ssm_step(cfg, **{k: (v[:, t] if v.dim() > 1 else v) for k, v in L.items()}, S=S)
+    wy, wS, _, ye, E = plain.scan(**L)
+    _near(S, wS, E)
+    _near(y, wy[:, -1], ye[:, -1])
+    assert float((S.cpu().double() - wS).norm() / wS.norm()) < 1e-5
+
+
 CONV = [(1, 1, 1, 2), (2, 70, 6, 3), (1, 40, 12, 4), (1, 2, 8, 4), (2, 3, 16, 4), (3, 33, 24, 3), (2, 65, 17, 4), (2, 130, 520, 2), (1, 31, 7, 3)]
 
 
