@@ -302,7 +302,8 @@ ramnet_status ramnet_decode_step(const ramnet_config* cfg, int32_t B, int32_t H,
  * not describe them; the definitions are those below.  Inputs are values that have already
  * been projected.  Shapes name contiguous last dimensions; per-token inputs take element
  * strides (as ramnet_strides) and need only element alignment, so slices of one wide
- * projection are read in place.  Non-finite inputs spread within their head or row (in
+ * projection are read in place.  Outputs share no memory with inputs, but for states where that
+ * is said, and state arrays start on 16 bytes, as y does.  Non-finite inputs spread within their head or row (in
  * ramnet_ssm_forward also to the up to 63 tokens before them); tokens that a sequence does not
  * have (see `lengths`) may hold anything.
  */
@@ -331,9 +332,10 @@ typedef struct {
  *           hands S_in on.
  *   S_in  [B,H,N,P] fp32 or NULL (zeros);  S_out [B,H,N,P] fp32 final state, may alias S_in
  *   y  [B,T,H,P] out_dt, dense
- *   workspace  device scratch of ramnet_ssm_workspace_bytes() bytes, 16-byte aligned (NULL if
- *           that is 0); not used by other work during the call
- * The state is fp32, and every sum has a fixed order: the same call gives the same bits.
+ *   workspace  device scratch of ramnet_ssm_workspace_bytes() bytes, 16-byte aligned; not used
+ *           by other work during the call, nor by a graph that may be replayed beside it
+ * The state is fp32, and every sum has a fixed order: the same call gives the same bits.  Waits
+ * on the device are bounded (2 s); one that runs out is reported by ramnet_sync_status.
  * Errors: INVALID_ARG (sizes, NULL, negative strides, alignment, small workspace).
  */
 size_t ramnet_ssm_workspace_bytes(const ramnet_ssm_config* cfg, int32_t B, int32_t T);

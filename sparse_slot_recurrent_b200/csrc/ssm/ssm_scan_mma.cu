@@ -9,26 +9,32 @@
 //   G^T [j,i] = B C^T      bf16, both from shared memory, M = 64
 //   Ya  [p,i] = X^T W^T    W[i,j] = exp(a_i - a_j) d_j G[i,j] (+ D on the diagonal) as two bf16 pieces in shared
 //                          memory, one product per head with the other heads' lanes switched off
-//   Yb  [p,i] = S^T C^T    tf32: S^T in tensor memory as it is, C widened to 32 bits in shared memory
+//   Yb  [p,i] = S^T C^T    S^T in tensor memory as two bf16 pieces
 //   dS  [p,n] = Xw^T B     Xw = exp(a_63 - a_j) d_j x_j in tensor memory as three bf16 pieces
 // and y^T = exp(a_i) Yb + Ya.  The tiles of x, B and C are used as they arrive by TMA, B and C in both
 // roles; x is transposed on the way to registers (ldmatrix.trans) and y on the way back.
 //
 // Precision.  The state itself stays in fp32 registers and takes dS with one fused multiply-add
 // per chunk (the tensor core's accumulation would shave a bit off a long-lived state every
-// chunk).  Xw is exact in three pieces of 8 bits.  As operands of a bf16 result W carries 16 bits and S 11: 2^-16 and
-// 2^-10 of each value, against the result's own 2^-9.  Sums of d A are taken in 64 bits; a_i - a_j is the
+// chunk).  Xw is exact in three pieces of 8 bits.  As operands of a bf16 result W and S carry two pieces: 2^-16 of each
+// value, against the result's own 2^-9.  Sums of d A are taken in 64 bits; a_i - a_j is the
 // difference of two float pairs within a block of 16 tokens, and between blocks a product of factors that meet at
 // block ends, so strong decay early in a chunk costs later tokens nothing.
 //
 // Work split.  A first small launch turns dt into step sizes and decays by chunk (k_ssm_decay).  Then one CTA per
 // (sequence, 128 channels, segment of the sequence), chunks in order, warps by role:
-//   0-7   operands: Xw and W, C in 32 bits;   8-15  state (32 channels x N/2 values each) and outputs;
-//   16    TMA loads and stores;  18 issues G and dS, 19 Yb and Ya.
-// The state's chain Y -> outputs read -> state stored -> Yb -> Y is what a chunk cannot go below; the rest overlaps.
-// The code of all roles has to stay within the instruction cache (about 32 KB of loops here): unrolling them fully
-// made every role wait for instructions and cost a third of the speed.
-// Bound: issue slots of the elementwise work, and the tensor pipe (about 1900 cycles per chunk at N = 128).
+//   0-7   operands: W, X^T, Xw, then half of the outputs;   8-15  state (32 channels x N/2 values each), half of the outputs;
+//   16    TMA loads and stores;  18 issues G and dS, 19 Ya and Yb.
+// The loops over chunks chain W -> Ya, Yb -> outputs and state -> Yb; the rest overlaps.  Launches follow one another as
+// programmatic dependents.
+//
+// The code of all roles has to stay within the instruction cache: with the loops fully unrolled (72 KB) every role
+// waited for instructions and a prompt took a third longer; unrolling W alone costs 3%.
+// Measured, B4 T16384 H16 P128 N128: 315 us (574 MB: 87 us at the copy bandwidth; token by token in registers 14 ms).
+// About 3700 cycles per chunk, of which the tensor pipe works 1900, shared memory 2100, HBM 1400.  Bound: the
+// operand warps of the first quadrant, whose diagonal and off-diagonal blocks of W take 1300 cycles of issue and latency
+// between a chunk's G and its Ya.
+// B8 T4096 H8 P128 N128: 97 us with 2 segments per sequence; B6 T1021 H24 P64 N64 in 2 groups: 39 us.
 #include "ssm_mma.cuh"
 
 namespace ramnet {
