@@ -184,6 +184,7 @@ cudaError_t go(const ConvParams& p, cudaStream_t s)
 {
     const int ncv = p.C / V;
     // Long runs read fewer rows twice and load their weights less often; short ones where those would leave SMs idle.
+    // (B4 T16384 C2304 bf16: 120 us in runs of 64, 155 in runs of 16; B1 T4096: 17 and 15.)
     int run = kRunLong;
     while (run > kRunShort && static_cast<int64_t>(ncv) * p.B * ((p.T + run - 1) / run) < 2ll * 148 * 640) run /= 2;
     const int64_t work = static_cast<int64_t>(ncv) * p.B * ((p.T + run - 1) / run);

@@ -141,7 +141,9 @@ cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t stream);
 cudaError_t launch_ssm_step(const SsmStepParams& p, cudaStream_t stream);
 cudaError_t launch_norm_gate(const NormParams& p, cudaStream_t stream);
 
+// How sequences are cut by the tensor-core form and by the token-by-token form (launch_ssm_scan sets p.split).
 SsmSplit ssm_split(int B, int T, int H, int G, int P);
+SsmSplit ssm_split_plain(int B, int T, int H, int N, int P);
 cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t stream);
 cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t stream);
 // The tensor-core form, for the types, sizes and layouts it takes.

@@ -75,18 +75,21 @@ bool take_strides(const ramnet_strides* s, int64_t B, int64_t T, int64_t H, int6
 size_t state_bytes(const ramnet_ssm_config* c, int64_t B) { return sizeof(float) * B * c->H * c->N * c->P; }
 
 // The workspace: step sizes and decays by chunk of 64 tokens, then, where sequences are cut, the pieces' states
-// and their decays.
+// and their decays; room for either form's cut.
 struct Workspace {
     size_t state_off, decay_off, total;
 };
 
-Workspace ssm_workspace(const ramnet_ssm_config* c, int64_t B, int64_t T, const ramnet::SsmSplit& split)
+Workspace ssm_workspace(const ramnet_ssm_config* c, int64_t B, int64_t T)
 {
     Workspace w;
     const size_t heads = static_cast<size_t>(B) * c->H;
+    size_t slots = 0;
+    for (const ramnet::SsmSplit& s : {ramnet::ssm_split(B, T, c->H, c->G, c->P), ramnet::ssm_split_plain(B, T, c->H, c->N, c->P)})
+        if (s.nseg > 1 && static_cast<size_t>(s.slots()) > slots) slots = s.slots();
     w.state_off = heads * ((T + ramnet::kChunk - 1) / ramnet::kChunk) * sizeof(ramnet::ChunkTok);
-    w.decay_off = w.state_off + (split.nseg > 1 ? state_bytes(c, B) * split.slots() : 0);
-    w.total = w.decay_off + (split.nseg > 1 ? sizeof(float) * heads * split.pieces() : 0);
+    w.decay_off = w.state_off + state_bytes(c, B) * slots;
+    w.total = w.decay_off + sizeof(float) * heads * slots;
     return w;
 }
 
@@ -98,7 +101,7 @@ size_t ramnet_ssm_workspace_bytes(const ramnet_ssm_config* cfg, int32_t B, int32
 {
     ramnet::set_last_error(RAMNET_OK, "");
     if (check_ssm(cfg, B, T) != RAMNET_OK) return 0;
-    return ssm_workspace(cfg, B, T, ramnet::ssm_split(B, T, cfg->H, cfg->G, cfg->P)).total;
+    return ssm_workspace(cfg, B, T).total;
 }
 
 ramnet_status ramnet_ssm_forward(const ramnet_ssm_config* cfg, int32_t B, int32_t T, ramnet_dtype in_dt, const void* x,
@@ -129,8 +132,7 @@ ramnet_status ramnet_ssm_forward(const ramnet_ssm_config* cfg, int32_t B, int32_
     MAY(S_in, 16);
     NEED(y, 16);
     NEED(S_out, 16);
-    p.split = ramnet::ssm_split(B, T, cfg->H, cfg->G, cfg->P);
-    const Workspace ws = ssm_workspace(cfg, B, T, p.split);
+    const Workspace ws = ssm_workspace(cfg, B, T);
     NEED(workspace, 16);
     CHECK(workspace_bytes >= ws.total, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.total);
     unsigned char* base = static_cast<unsigned char*>(workspace);

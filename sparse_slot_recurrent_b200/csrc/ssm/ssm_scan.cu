@@ -9,7 +9,7 @@
 // k_ssm_tile, for heads of at least 64 x 32 values or so: a thread holds 8 state values of 4 channels, so that a token's
 // loads from shared memory (5 x 16 bytes) serve 96 multiply-adds, taken in pairs; the lane sum scatters 4 channels while it
 // adds, and y leaves through shared memory.  (k_ssm_scan moves four times the shared memory per value: 9.8 ms for
-// B4 T16384 H16 P128 N128 in fp32, against 5.2 ms.)
+// B4 T16384 H16 P128 N128 in fp32, against 5.0 ms.)
 // Bound: fp32 issue (3 N P per token-head) and, with few heads, the latency of the token chain.
 #include "pairs.cuh"
 #include "ssm_common.cuh"
@@ -414,8 +414,12 @@ cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t s)
     return cudaSuccess;
 }
 
-// As many segments as fill 148 SMs with one block of 128 channels each, none shorter than 256
-// tokens; and where the segments before the last leave SMs idle in the first launch, pieces of them.
+// As many segments as fill 148 SMs with one block of 128 channels each, none shorter than 256 tokens, and none at all
+// below 768 tokens, where two more launches cost more than they save.  (H2 P128 N128, whole against cut: T512 25 us and 31,
+// T1024 39 and 31, T4096 126 and 32; B4 H16 T16384 524 and 315.)  Where the segments before the last leave SMs idle in
+// the first launch, pieces of them run there: halving them saves a chunk's time for every 64 tokens (about a
+// microsecond), and the chain takes about a quarter of that per piece more.  (B6 T1021 H24 P64 N64: 44 us with whole
+// segments, 38 with halves; but H2 T4096, 16 segments of 256 tokens: 32 us whole, 42 in quarters.)
 SsmSplit ssm_split(int B, int T, int H, int G, int P)
 {
     const int64_t units = static_cast<int64_t>(B) * G * ((static_cast<int64_t>(H / G) * P + 127) / 128);
@@ -423,11 +427,30 @@ SsmSplit ssm_split(int B, int T, int H, int G, int P)
     const int64_t most = T / 256;
     n = n < most ? n : most;
     SsmSplit s{1, T, 1};
-    if (n <= 1) return s;
+    if (n <= 1 || most <= 2) return s;
     s.seg_len = static_cast<int>((T + n - 1) / n + 63) / 64 * 64;
     s.nseg = (T + s.seg_len - 1) / s.seg_len;
     if (s.nseg <= 1) return SsmSplit{1, T, 1};
-    while (units * (s.nseg - 1) * s.sub * 2 <= 148 && s.seg_len % (128 * s.sub) == 0) s.sub *= 2;
+    while (units * s.pieces() * 2 <= 148 && s.seg_len % (128 * s.sub) == 0 && s.seg_len / (128 * s.sub) * 4 >= s.pieces()) s.sub *= 2;
+    return s;
+}
+
+// The same for the token-by-token form, where a token costs a block its latency whatever else runs: segments from 64
+// tokens on while there are no more than 4 blocks per SM, but none where that leaves only two (the first launch and the
+// chain then cost what they save).  Whole against cut, fp32: B2 T333 H5 P32 N16 59 us and 28, T2048 341 and 36;
+// B4 T4096 H20 P64 N64 853 and 454; H16 P128 N128 T16384 B1 4074 and 1445, B4 (in two) 5030 and 5390.
+SsmSplit ssm_split_plain(int B, int T, int H, int N, int P)
+{
+    int most = 4096 / N;
+    while (most > P) most /= 2;  // channels per block
+    const int64_t units = static_cast<int64_t>(B) * H * (P / most);
+    int64_t n = 4 * 148 / units;
+    n = n < T / 64 ? n : T / 64;
+    if (n > 148) n = 148;
+    SsmSplit s{1, T, 1};
+    if (n <= 2) return s;
+    s.seg_len = static_cast<int>((T + n - 1) / n + 15) / 16 * 16;
+    s.nseg = (T + s.seg_len - 1) / s.seg_len;
     return s;
 }
 
@@ -443,10 +466,17 @@ cudaError_t launch_ssm_plain(const SsmParams& p, cudaStream_t s)
     }
 }
 
+// The tensor-core form, but for a few tokens of a few heads: those are through, token by token, before a chunk of 64 is.
+// (H16 P128 N128, one launch against two: B4 T16 14 us and 18, T64 27 and 23; but B9 T32 28 and 18, B64 T16 85 and 61.)
 cudaError_t launch_ssm_scan(const SsmParams& p, cudaStream_t s)
 {
-    if (ssm_mma_takes(p)) return launch_ssm_mma(p, s);
     SsmParams q = p;
+    const bool few = p.T <= 16 && static_cast<int64_t>(p.B) * p.H * p.P <= 148 * 128;
+    if (!few && ssm_mma_takes(p)) {
+        q.split = ssm_split(p.B, p.T, p.H, p.G, p.P);
+        return launch_ssm_mma(q, s);
+    }
+    q.split = ssm_split_plain(p.B, p.T, p.H, p.N, p.P);
     q.toks = nullptr;
     return launch_ssm_plain(q, s);
 }

@@ -764,6 +764,8 @@ bool ok_stride(int64_t n, int64_t size) { return size == 1 || (n > 0 && n % 8 ==
 
 }  // namespace
 
+// (N = 256 would take 512 columns of tensor memory for the state's pieces and dS alone, and P = 16 eight copies of W, 128
+// KB: those sizes, like fp32 and layouts that TMA does not read, go token by token.)
 bool ssm_mma_takes(const SsmParams& p)
 {
     if (!p.in_bf16 || !p.out_bf16 || p.P < 32 || p.N > 128) return false;
