@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(N / 8 * (PT / 4)) k_ssm_tile(SsmParams p)
     constexpr int NG = N / 8, TH = NG * (PT / 4);
     constexpr int LB = kTok * N / TH, LX = kTok * PT / TH;
     static_assert(NG <= 32 && LB * TH == kTok * N && LX * TH == kTok * PT, "shape");
-    __shared__ __align__(16) float sB[kTok * N], sC[OUT ? kTok * N : 4], sX[kTok * PT], sY[OUT ? kTok * PT : 4], sA[kTok], sD[kTok];
+    __shared__ __align__(16) float sB[kTok * N], sC[OUT ? kTok * N : 4], sX[kTok * PT], sY[OUT ? kTok * PT : 4];
+    __shared__ float2 sA[kTok];  // a token's decay and step size
     const int seg = blockIdx.y, tid = threadIdx.x;
     const int ptiles = p.P / PT;
     const int tile = static_cast<int>(blockIdx.x % ptiles);
@@ -221,64 +222,77 @@ __global__ void __launch_bounds__(N / 8 * (PT / 4)) k_ssm_tile(SsmParams p)
         }
 #pragma unroll
         for (int k = 0; k < LX; ++k) sX[k * TH + tid] = value_of<BF>(vX[k]);
-        if (tid < nt) {
-            const float d = step_size(value_of<BF>(vD), bias, p.softplus, p.dt_min, p.dt_max);
-            const double l = static_cast<double>(d) * A;
-            sD[tid] = d;
-            sA[tid] = exp2_of(l * 1.4426950408889634074);  // rounded once from 64 bits, as in k_ssm_scan
-            logdecay += l;
+        if (tid < kTok) {
+            float2 ad = make_float2(1.0f, 0.0f);  // a token that is not there changes nothing
+            if (tid < nt) {
+                const float d = step_size(value_of<BF>(vD), bias, p.softplus, p.dt_min, p.dt_max);
+                const double l = static_cast<double>(d) * A;
+                ad = make_float2(exp2_of(l * 1.4426950408889634074), d);  // rounded once from 64 bits, as in k_ssm_scan
+                logdecay += l;
+            }
+            sA[tid] = ad;
         }
         __syncthreads();
         if (t0 + kTok < r.last) fetch(t0 + kTok);
-#pragma unroll 2
-        for (int t = 0; t < nt; ++t) {
-            const float av = sA[t], dv = sD[t];
-            const float4 xv = *reinterpret_cast<const float4*>(sX + t * PT + pl);
-            const F2 a = f2(av, av);
-            const F2 u[4] = {f2(dv * xv.x, dv * xv.x), f2(dv * xv.y, dv * xv.y), f2(dv * xv.z, dv * xv.z), f2(dv * xv.w, dv * xv.w)};
-            F2 y[4] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f), f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
+#pragma unroll 1
+        for (int t4 = 0; t4 < nt; t4 += 4) {
+            float v[16];  // this lane's part of y: 4 tokens x 4 channels
 #pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-                const float4 bv = *reinterpret_cast<const float4*>(sB + t * N + 4 * (s + NG * k2));
-                const F2 bb[2] = {f2(bv.x, bv.y), f2(bv.z, bv.w)};
-                F2 cc[2];
-                if (OUT) {
-                    const float4 cv = *reinterpret_cast<const float4*>(sC + t * N + 4 * (s + NG * k2));
-                    cc[0] = f2(cv.x, cv.y), cc[1] = f2(cv.z, cv.w);
-                }
+            for (int i = 0; i < 4; ++i) {
+                const int t = t4 + i;
+                const float2 ad = sA[t];
+                const float4 xv = *reinterpret_cast<const float4*>(sX + t * PT + pl);
+                const F2 a = f2(ad.x, ad.x);
+                const F2 u[4] = {f2(ad.y * xv.x, ad.y * xv.x), f2(ad.y * xv.y, ad.y * xv.y), f2(ad.y * xv.z, ad.y * xv.z), f2(ad.y * xv.w, ad.y * xv.w)};
+                F2 y[4] = {f2(0.0f, 0.0f), f2(0.0f, 0.0f), f2(0.0f, 0.0f), f2(0.0f, 0.0f)};
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        F2& v = S[2 * k2 + j][q];
-                        v = fma2(bb[j], u[q], mul2(a, v));
-                        if (OUT) y[q] = fma2(cc[j], v, y[q]);
+                for (int k2 = 0; k2 < 2; ++k2) {
+                    const float4 bv = *reinterpret_cast<const float4*>(sB + t * N + 4 * (s + NG * k2));
+                    const F2 bb[2] = {f2(bv.x, bv.y), f2(bv.z, bv.w)};
+                    F2 cc[2];
+                    if (OUT) {
+                        const float4 cv = *reinterpret_cast<const float4*>(sC + t * N + 4 * (s + NG * k2));
+                        cc[0] = f2(cv.x, cv.y), cc[1] = f2(cv.z, cv.w);
                     }
-            }
-            if (OUT) {
-                float v[4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            F2& w = S[2 * k2 + j][q];
+                            w = fma2(bb[j], u[q], mul2(a, w));
+                            if (OUT) y[q] = fma2(cc[j], w, y[q]);
+                        }
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float e, f;
                     un(y[q], e, f);
-                    v[q] = e + f;
+                    v[4 * i + q] = e + f;
                 }
-                // sums over the lanes of these channels: halves of the channels are handed over first, then whole lanes
-                const bool up = s & 1, up2 = s & 2;
-                float k0 = up ? v[2] : v[0], k1 = up ? v[3] : v[1];
-                k0 += __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 1);
-                k1 += __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 1);
-                int ch = up ? 2 : 0;
-                if constexpr (NG >= 4) {
-                    float k = up2 ? k1 : k0;
-                    k += __shfl_xor_sync(0xffffffffu, up2 ? k0 : k1, 2);
-                    ch += up2 ? 1 : 0;
+            }
+            if (OUT) {
+                // sums over the lanes of these channels: of two lanes each hands the other half of its values, then whole sums
+                constexpr int kHalvings = NG >= 16 ? 4 : NG == 8 ? 3 : NG == 4 ? 2 : 1;
+                int first = 0;  // of this lane's values among the 16
 #pragma unroll
-                    for (int o = 4; o < NG; o <<= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
-                    if (s < 4) sY[t * PT + pl + ch] = fmaf(skip, sX[t * PT + pl + ch], k);
-                } else {
-                    sY[t * PT + pl + ch] = fmaf(skip, sX[t * PT + pl + ch], k0);
-                    sY[t * PT + pl + ch + 1] = fmaf(skip, sX[t * PT + pl + ch + 1], k1);
+                for (int m = 0; m < kHalvings; ++m) {
+                    const int half = 8 >> m;
+                    const bool up = s & (1 << m);
+                    first += up ? half : 0;
+#pragma unroll
+                    for (int e = 0; e < half; ++e) {
+                        const float give = up ? v[e] : v[e + half];
+                        v[e] = (up ? v[e + half] : v[e]) + __shfl_xor_sync(0xffffffffu, give, 1 << m);
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o < NG; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                if (s < 16) {
+#pragma unroll
+                    for (int e = 0; e < (16 >> kHalvings); ++e) {
+                        const int at = (t4 + ((first + e) >> 2)) * PT + pl + ((first + e) & 3);
+                        sY[at] = fmaf(skip, sX[at], v[e]);
+                    }
                 }
             }
         }
