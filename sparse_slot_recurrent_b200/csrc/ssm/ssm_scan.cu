@@ -7,9 +7,10 @@
 // step sizes go through shared memory; while one is worked on, the next is on its way into registers.  Per token a
 // thread takes 3 NR multiply-adds and a log2(NS)-step lane sum.
 // k_ssm_tile, for heads of at least 64 x 32 values or so: a thread holds 8 state values of 4 channels, so that a token's
-// loads from shared memory (5 x 16 bytes) serve 96 multiply-adds, taken in pairs; the lane sum scatters 4 channels while it
+// loads from shared memory (5 x 16 bytes) serve 96 multiply-adds, taken in pairs; the lane sum scatters the channels while it
 // adds, and y leaves through shared memory.  (k_ssm_scan moves four times the shared memory per value: 9.8 ms for
-// B4 T16384 H16 P128 N128 in fp32, against 5.0 ms.)
+// B4 T16384 H16 P128 N128 in fp32, against 3.7 ms.)  The lane sums take four tokens at once: one at a time their shuffles
+// were each token's latency (5.0 ms).
 // Bound: fp32 issue (3 N P per token-head) and, with few heads, the latency of the token chain.
 #include "pairs.cuh"
 #include "ssm_common.cuh"
@@ -185,28 +186,35 @@ __global__ void __launch_bounds__(N / 8 * (PT / 4)) k_ssm_tile(SsmParams p)
         }
         S[k][0] = f2(lo.x, hi.x), S[k][1] = f2(lo.y, hi.y), S[k][2] = f2(lo.z, hi.z), S[k][3] = f2(lo.w, hi.w);
     }
-    // the block of tokens from t0, into registers (tokens that are not there as zeros)
+    // The block of tokens from t0, into registers (tokens that are not there as zeros).  Value k of a thread lies a fixed
+    // number of tokens and columns behind its first.
     uint32_t vB[LB], vC[LB], vX[LX], vD = 0;
+    const int64_t oB = b * p.bs.b + g * p.bs.h + tid % N + (r.first + tid / N) * p.bs.t, oC = b * p.cs.b + g * p.cs.h + tid % N + (r.first + tid / N) * p.cs.t;
+    const int64_t oX = b * p.xs.b + h * p.xs.h + tile * PT + tid % PT + (r.first + tid / PT) * p.xs.t, oD = b * p.dts.b + h * p.dts.h + (r.first + tid) * p.dts.t;
     auto fetch = [&](int t0) {
+        const int64_t on = t0 - r.first;
+        const int left = r.last - t0;
+        const int64_t fB = oB + on * p.bs.t, fC = oC + on * p.cs.t, fX = oX + on * p.xs.t;
 #pragma unroll
         for (int k = 0; k < LB; ++k) {
-            const int i = k * TH + tid, t = t0 + i / N, n = i % N;
-            vB[k] = t < r.last ? bits_at<BF>(p.Bm, b * p.bs.b + t * p.bs.t + g * p.bs.h + n) : 0u;
-            if (OUT) vC[k] = t < r.last ? bits_at<BF>(p.Cm, b * p.cs.b + t * p.cs.t + g * p.cs.h + n) : 0u;
+            const int t = k * TH / N, n = k * TH % N;
+            vB[k] = t + tid / N < left ? bits_at<BF>(p.Bm, fB + t * p.bs.t + n) : 0u;
+            if (OUT) vC[k] = t + tid / N < left ? bits_at<BF>(p.Cm, fC + t * p.cs.t + n) : 0u;
         }
 #pragma unroll
         for (int k = 0; k < LX; ++k) {
-            const int i = k * TH + tid, t = t0 + i / PT;
-            vX[k] = t < r.last ? bits_at<BF>(p.x, b * p.xs.b + t * p.xs.t + h * p.xs.h + tile * PT + i % PT) : 0u;
+            const int t = k * TH / PT, c = k * TH % PT;
+            vX[k] = t + tid / PT < left ? bits_at<BF>(p.x, fX + t * p.xs.t + c) : 0u;
         }
-        if (tid < kTok && t0 + tid < r.last) vD = bits_at<BF>(p.dt, b * p.dts.b + (t0 + tid) * p.dts.t + h * p.dts.h);
+        if (tid < kTok && tid < left) vD = bits_at<BF>(p.dt, oD + on * p.dts.t);
     };
+    const int64_t yrow = static_cast<int64_t>(p.H) * p.P, oY = (b * p.T + tid / PT) * yrow + static_cast<int64_t>(h) * p.P + tile * PT + tid % PT;
     auto leave = [&](int t0, int nt) {  // y of the block of nt tokens from t0
+        const int64_t to = oY + t0 * yrow;
 #pragma unroll
         for (int k = 0; k < LX; ++k) {
-            const int i = k * TH + tid;
-            if (i / PT < nt)
-                store_out(p.y, static_cast<size_t>(((b * p.T + t0 + i / PT) * p.H + h) * p.P + tile * PT + i % PT), sY[i], p.out_bf16);
+            const int t = k * TH / PT, c = k * TH % PT;
+            if (t + tid / PT < nt) store_out(p.y, static_cast<size_t>(to + t * yrow + c), sY[k * TH + tid], p.out_bf16);
         }
     };
     double logdecay = 0.0;  // of this thread's tokens (the first kTok threads)
@@ -450,17 +458,20 @@ SsmSplit ssm_split(int B, int T, int H, int G, int P)
 }
 
 // The same for the token-by-token form, where a token costs a block its latency whatever else runs: segments from 64
-// tokens on while there are no more than 4 blocks per SM, but none where that leaves only two (the first launch and the
-// chain then cost what they save).  Whole against cut, fp32: B2 T333 H5 P32 N16 59 us and 28, T2048 341 and 36;
-// B4 T4096 H20 P64 N64 853 and 454; H16 P128 N128 T16384 B1 4074 and 1445, B4 (in two) 5030 and 5390.
+// tokens on while there are no more than 512 threads per SM, but none where that leaves only two (the first launch and the
+// chain then cost what they save), and 64 at most, for the chain.  Whole against cut, fp32: B2 T333 H5 P32 N16 59 us and
+// 28, T2048 341 and 36; B4 T4096 H20 P64 N64 853 and 397; H16 P128 N128 T16384 B1 4.1 ms and 1.2, B4 (in two) 5.0
+// and 5.4.  Up to 256 threads: 164 us instead of 111 for B5 T11720 H5 P16 N16; up to 1024: 107 instead of 88 for B5 T276
+// H42 P16 N256.  118 segments: 99 us instead of 95 for B5 T7669 H2 P16 N128.
 SsmSplit ssm_split_plain(int B, int T, int H, int N, int P)
 {
     int most = 4096 / N;
     while (most > P) most /= 2;  // channels per block
+    const int threads = N * most > 1024 ? N * most / 32 : 64;
     const int64_t units = static_cast<int64_t>(B) * H * (P / most);
-    int64_t n = 4 * 148 / units;
+    int64_t n = 148 * 512 / (units * threads);
     n = n < T / 64 ? n : T / 64;
-    if (n > 148) n = 148;
+    if (n > 64) n = 64;
     SsmSplit s{1, T, 1};
     if (n <= 2) return s;
     s.seg_len = static_cast<int>((T + n - 1) / n + 15) / 16 * 16;
