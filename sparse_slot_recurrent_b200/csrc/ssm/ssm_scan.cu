@@ -335,7 +335,8 @@ __global__ void __launch_bounds__(N / 8 * (PT / 4)) k_ssm_tile(SsmParams p)
 
 // Turns what the pieces add into the states the segments start from, in token order; four
 // neighbouring state values per thread, one (sequence, head) per blockIdx.y.  With chunk totals the
-// pieces' decays come from those, else from seg_decay.
+// pieces' decays come from those, else from seg_decay.  Bound: latency; the next piece's values are asked for one ahead, the
+// first before the decays are summed (B8 T4096 H8 P128 N128: 95 us in all instead of 96).
 __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
 {
     __shared__ float decay[256];
@@ -345,6 +346,12 @@ __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
     const int e = blockIdx.x * 256 + threadIdx.x;
     const int64_t bh = blockIdx.y;
     const int n = p.split.pieces(), sub = p.split.sub;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), add = s;
+    float4* at = reinterpret_cast<float4*>(p.seg_state) + bh * p.split.slots() * np4 + e;
+    if (e < np4) {  // on their way while the decays are summed
+        if (p.S_in) s = reinterpret_cast<const float4*>(p.S_in)[bh * np4 + e];
+        add = *at;
+    }
     for (int k = threadIdx.x >> 5; k < n; k += 8) {  // a warp per piece
         if (p.toks) {
             const int chunks = (p.T + kChunk - 1) / kChunk, per = p.split.piece_len() / kChunk;
@@ -361,14 +368,14 @@ __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
     }
     __syncthreads();
     if (e >= np4) return;
-    float4 s = p.S_in ? reinterpret_cast<const float4*>(p.S_in)[bh * np4 + e] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float4* at = reinterpret_cast<float4*>(p.seg_state) + bh * p.split.slots() * np4 + e;
 #pragma unroll 4
     for (int k = 0; k < n; ++k, at += np4) {
-        const float4 add = *at;
+        float4 next = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (k + 1 < n) next = at[np4];
         const float d = decay[k];
         if (k % sub == 0) *at = s;
         s = make_float4(fmaf(d, s.x, add.x), fmaf(d, s.y, add.y), fmaf(d, s.z, add.z), fmaf(d, s.w, add.w));
+        add = next;
     }
     *at = s;
 }
@@ -438,7 +445,7 @@ cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t s)
 
 // As many segments as fill 148 SMs with one block of 128 channels each, none shorter than 256 tokens, and none at all
 // below 768 tokens, where two more launches cost more than they save.  (H2 P128 N128, whole against cut: T512 25 us and 31,
-// T1024 39 and 31, T4096 126 and 32; B4 H16 T16384 524 and 315.)  Where the segments before the last leave SMs idle in
+// T1024 39 and 31, T4096 126 and 32; B1 H32 T4096 130 and 70.)  Where the segments before the last leave SMs idle in
 // the first launch, pieces of them run there: halving them saves a chunk's time for every 64 tokens (about a
 // microsecond), and the chain takes about a quarter of that per piece more.  (B6 T1021 H24 P64 N64: 44 us with whole
 // segments, 38 with halves; but H2 T4096, 16 segments of 256 tokens: 32 us whole, 42 in quarters.)

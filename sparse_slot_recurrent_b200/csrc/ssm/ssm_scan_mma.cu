@@ -34,7 +34,7 @@
 // About 3700 cycles per chunk, of which the tensor pipe works 1900, shared memory 2100, HBM 1400.  Bound: the
 // operand warps of the first quadrant, whose diagonal and off-diagonal blocks of W take 1300 cycles of issue and latency
 // between a chunk's G and its Ya.
-// B8 T4096 H8 P128 N128: 97 us with 2 segments per sequence; B6 T1021 H24 P64 N64 in 2 groups: 39 us.
+// B8 T4096 H8 P128 N128: 95 us with 2 segments per sequence; B6 T1021 H24 P64 N64 in 2 groups: 37 us.
 #include "ssm_mma.cuh"
 
 namespace ramnet {
