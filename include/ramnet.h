@@ -309,7 +309,8 @@ ramnet_status ramnet_decode_step(const ramnet_config* cfg, int32_t B, int32_t H,
  */
 
 /* H heads of P channels with N state values per channel; head h uses the B and C vectors of
- * group h / (H/G).  Limits: P and N in {16, 32, 64, 128, 256}, G >= 1 divides H. */
+ * group h / (H/G).  Limits: P and N in {16, 32, 64, 128, 256}, G >= 1 divides H,
+ * B*T*H < 2^31, B*H < 2^27, T <= 2^30. */
 typedef struct {
     int32_t H, G, N, P;
     int32_t dt_softplus;   /* 1: step size softplus(dt + dt_bias), 0: dt + dt_bias          */
@@ -368,7 +369,7 @@ ramnet_status ramnet_ssm_step(const ramnet_ssm_config* cfg, int32_t B, ramnet_dt
  *   state_in, state_out [B,W-1,C] in_dt or NULL: the last W-1 inputs before and after the call;
  *           may be the same array
  *   y [B,T,C] out_dt, dense
- * Limits: 2 <= W <= 4.  Errors: INVALID_ARG.
+ * Limits: 2 <= W <= 4, B*T < 2^31, B*C < 2^31, T <= 2^30.  Errors: INVALID_ARG.
  */
 ramnet_status ramnet_conv_forward(int32_t B, int32_t T, int32_t C, int32_t W, ramnet_dtype in_dt,
                                   const void* x, int64_t x_b, int64_t x_t, const float* w,
@@ -388,7 +389,7 @@ ramnet_status ramnet_conv_step(int32_t B, int32_t C, int32_t W, ramnet_dtype in_
  *     gate_first == 0:  y = x / sqrt(mean_group(x^2) + eps) * w * silu(z)
  *   x, z [R,D] in_dt with row strides x_r, z_r in elements (z NULL: no gate);  w [D] fp32 or
  *   NULL (ones);  y [R,D] out_dt, dense
- * Errors: INVALID_ARG.
+ * Limits: R*groups < 2^31, D <= 2^30.  Errors: INVALID_ARG.
  */
 ramnet_status ramnet_norm_gate(int64_t R, int32_t D, int32_t groups, ramnet_dtype in_dt, const void* x,
                                int64_t x_r, const void* z, int64_t z_r, const float* w, float eps,

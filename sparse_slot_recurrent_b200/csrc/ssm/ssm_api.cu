@@ -43,6 +43,9 @@ size_t elem(ramnet_dtype d) { return d == RAMNET_BF16 ? 2 : 4; }
     } while (0)
 #define MAY(p, n) CHECK((p) == nullptr || aligned(p, n), "%s not %zu-byte aligned", #p, (size_t)(n))
 
+// Longest sequence or row: indices may run a block past its end without leaving 32 bits.
+constexpr int64_t kLongest = 1ll << 30;
+
 bool side(int32_t n) { return n == 16 || n == 32 || n == 64 || n == 128 || n == 256; }
 
 ramnet_status check_ssm(const ramnet_ssm_config* c, int64_t B, int64_t T)
@@ -55,6 +58,7 @@ ramnet_status check_ssm(const ramnet_ssm_config* c, int64_t B, int64_t T)
     CHECK(B >= 1 && T >= 1, "B and T must be >= 1");
     // (B*H first: the product of all three could pass 64 bits)
     CHECK(B * c->H <= (1ll << 27) - 1 && B * c->H * T <= (1ll << 31) - 1, "B*T*H too large");
+    CHECK(T <= kLongest, "T too large");
     return RAMNET_OK;
 }
 
@@ -193,6 +197,7 @@ ramnet_status ramnet_conv_forward(int32_t B, int32_t T, int32_t C, int32_t W, ra
               static_cast<int64_t>(B) * C <= (1ll << 31) - 1 &&
               static_cast<double>(B) * C * ((static_cast<int64_t>(T) + 15) / 16) <= 1.0e11,
           "B*T*C too large");
+    CHECK(T <= kLongest, "T too large");
     CHECK(W >= 2 && W <= 4, "W=%d outside [2,4]", W);
     CHECK(valid_dtype(in_dt) && valid_dtype(out_dt), "bad dtype");
     ramnet::Str3 xs;
@@ -239,6 +244,7 @@ ramnet_status ramnet_norm_gate(int64_t R, int32_t D, int32_t groups, ramnet_dtyp
 {
     ramnet::set_last_error(RAMNET_OK, "");
     CHECK(R >= 1 && D >= 1, "R and D must be >= 1");
+    CHECK(D <= kLongest, "D too large");
     CHECK(groups >= 1 && D % groups == 0, "groups=%d does not divide D=%d", groups, D);
     CHECK(R <= ((1ll << 31) - 1) / groups, "R*groups too large");
     CHECK(valid_dtype(in_dt) && valid_dtype(out_dt), "bad dtype");

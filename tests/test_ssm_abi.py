@@ -42,7 +42,8 @@ def test_bad_layers_refused(lib, kw):
 
 
 @pytest.mark.parametrize("kw,word", [
-    (dict(B=0), "B"), (dict(T=0), "T"), (dict(B=1 << 30, T=1 << 30), "large"), (dict(dt=7), "dtype"), (dict(od=9), "dtype"),
+    (dict(B=0), "B"), (dict(T=0), "T"), (dict(B=1 << 30, T=1 << 30), "large"), (dict(cfg=_cfg(H=1, G=1), B=1, T=(1 << 30) + 1), "large"),
+    (dict(dt=7), "dtype"), (dict(od=9), "dtype"),
     (dict(x=None), "x"), (dict(x=FAKE + 1), "aligned"), (dict(dt_ptr=None), "dt"), (dict(A=None), "A"), (dict(A=FAKE + 2), "A"),
     (dict(Bm=None), "Bm"), (dict(Cm=None), "Cm"), (dict(Cm=FAKE + 3), "Cm"), (dict(D=FAKE + 2), "D"), (dict(bias=FAKE + 1), "bias"),
     (dict(lengths=FAKE + 2), "lengths"), (dict(S_in=FAKE + 4), "S_in"), (dict(y=None), "y"), (dict(y=FAKE + 8), "y"),
@@ -78,7 +79,8 @@ def test_bad_conv_arguments_refused(lib):
     for kw in (dict(B=0), dict(T=0), dict(C=0), dict(W=1), dict(W=5), dict(dt=3), dict(od=3), dict(x=None), dict(x=FAKE + 1),
                dict(xb=-1), dict(xt=-8), dict(w=None), dict(w=FAKE + 2), dict(bias=FAKE + 1), dict(lengths=FAKE + 1),
                dict(si=FAKE + 2), dict(so=FAKE + 4), dict(y=None), dict(y=FAKE + 4), dict(B=1 << 20, C=1 << 20),
-               dict(B=1 << 16, T=1 << 16), dict(B=1 << 10, T=1 << 20, C=1 << 20)):
+               dict(B=1 << 16, T=1 << 16), dict(B=1 << 10, T=1 << 20, C=1 << 20),
+               dict(B=1, T=(1 << 30) + 1, C=1)):
         assert _conv(lib, **kw) == BAD, kw
     step = lambda B=2, C=8, W=4, dt=BF, x=FAKE, xb=8, w=FAKE, st=FAKE, y=FAKE, od=BF: lib.ramnet_conv_step(  # noqa: E731
         B, C, W, dt, x, xb, w, None, 1, st, y, od, None)
@@ -92,7 +94,7 @@ def test_bad_norm_arguments_refused(lib):
         R, D, groups, dt, x, xr, z, zr, w, eps, 1, y, od, None)
     for kw in (dict(R=0), dict(D=0), dict(groups=0), dict(groups=3), dict(dt=4), dict(od=4), dict(x=None), dict(x=FAKE + 1), dict(xr=-1),
                dict(z=FAKE + 1), dict(zr=-4), dict(w=FAKE + 4), dict(eps=-1.0), dict(eps=float("nan")), dict(y=None), dict(y=FAKE + 2),
-               dict(R=1 << 31)):
+               dict(R=1 << 31), dict(R=1, D=(1 << 30) + 2)):
         assert norm(**kw) == BAD, kw
 
 
