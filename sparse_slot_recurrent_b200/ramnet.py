@@ -407,10 +407,21 @@ def _input(x, name):
     return code, x.get_device()
 
 
-def _output(y, name, shape, out_dtype, x, dev):
+def _empty(shape, dtype, device, stream):
+    """A new tensor, in memory that is ordered on the stream that will write it: memory of the current stream may
+    still be in use there by work that came before."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _output(y, name, shape, out_dtype, x, dev, stream):
     """The output tensor (allocated if not given) and its dtype code."""
     if y is None:
-        y = torch.empty(shape, dtype=x.dtype if out_dtype is None else out_dtype, device=x.device)
+        y = _empty(shape, x.dtype if out_dtype is None else out_dtype, x.device, stream)
     elif out_dtype is not None and y.dtype is not out_dtype:
         raise TypeError(f"{name} is {y.dtype}, out_dtype is {out_dtype}")
     else:
@@ -460,15 +471,12 @@ def ssm_forward(cfg: SsmConfig, x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=
     state = (B, cfg.H, cfg.N, cfg.P)
     plen = _dense_ptr(lengths, "lengths", (B,), torch.int32, dev)
     pin = _dense_ptr(S_in, "S_in", state, torch.float32, dev)
-    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev, stream)
     if S_out is None:
-        S_out = torch.empty(state, dtype=torch.float32, device=x.device)
+        S_out = _empty(state, torch.float32, x.device, stream)
     pout = _dense_ptr(S_out, "S_out", state, torch.float32, dev)
     if workspace is None:
-        workspace = torch.empty(ssm_workspace_bytes(cfg, B, T), dtype=torch.uint8, device=x.device)
-        if stream is not None:  # it is given back when this call returns, and the work may still be waiting
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                    torch.cuda.ExternalStream(int(stream), device=x.device))
+        workspace = _empty(ssm_workspace_bytes(cfg, B, T), torch.uint8, x.device, stream)
     elif not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous and on the device of x")
     _launch(dev, stream, load().ramnet_ssm_forward, cfg._ref, B, T, code, px, _strides_of(*x.stride()[:3]), pdt,
@@ -483,7 +491,7 @@ def ssm_step(cfg: SsmConfig, x, dt, A, Bm, Cm, S, D=None, dt_bias=None, out_dtyp
     code, dev, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
     B = x.shape[0]
     pS = _dense_ptr(S, "S", (B, cfg.H, cfg.N, cfg.P), torch.float32, dev)
-    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev, stream)
     (xb, xh, _), (db, dh), (bb, bg, _), (cb, cg, _) = x.stride(), dt.stride(), Bm.stride(), Cm.stride()
     _launch(dev, stream, load().ramnet_ssm_step, cfg._ref, B, code, px, _strides_of(xb, 0, xh), pdt, _strides_of(db, 0, dh), pA,
             pB, _strides_of(bb, 0, bg), pC, _strides_of(cb, 0, cg), pD, pbias, pS, y.data_ptr(), ycode)
@@ -500,9 +508,9 @@ def conv_forward(x, w, bias=None, silu=True, lengths=None, state_in=None, out_dt
     px, pw, pb = _rows_ptr(x, "x", x.shape, t, dev), _dense_ptr(w, "w", (C, W), f32, dev), _dense_ptr(bias, "bias", (C,), f32, dev)
     plen = _dense_ptr(lengths, "lengths", (B,), torch.int32, dev)
     pin = _dense_ptr(state_in, "state_in", (B, W - 1, C), t, dev)
-    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev, stream)
     if state_out is None:
-        state_out = torch.empty((B, W - 1, C), dtype=t, device=x.device)
+        state_out = _empty((B, W - 1, C), t, x.device, stream)
     pout = _dense_ptr(state_out, "state_out", (B, W - 1, C), t, dev)
     _launch(dev, stream, load().ramnet_conv_forward, B, T, C, W, code, px, x.stride(0), x.stride(1), pw, pb, bool(silu), plen, pin,
             y.data_ptr(), ycode, pout)
@@ -516,7 +524,7 @@ def conv_step(x, w, state, bias=None, silu=True, out_dtype=None, y=None, stream=
     (B, C), W, t, f32 = x.shape, w.shape[1], x.dtype, torch.float32
     px, pw, pb = _rows_ptr(x, "x", x.shape, t, dev), _dense_ptr(w, "w", (C, W), f32, dev), _dense_ptr(bias, "bias", (C,), f32, dev)
     ps = _dense_ptr(state, "state", (B, W - 1, C), t, dev)
-    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev, stream)
     _launch(dev, stream, load().ramnet_conv_step, B, C, W, code, px, x.stride(0), pw, pb, bool(silu), ps, y.data_ptr(), ycode)
     return y
 
@@ -529,7 +537,7 @@ def norm_gate(x, z=None, w=None, groups=1, eps=1e-6, gate_first=True, out_dtype=
     px = _rows_ptr(x, "x", x.shape, x.dtype, dev)
     pz, zs = (None, 0) if z is None else (_rows_ptr(z, "z", x.shape, x.dtype, dev), z.stride(0))
     pw = _dense_ptr(w, "w", (D,), torch.float32, dev)
-    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev)
+    y, ycode = _output(y, "y", x.shape, out_dtype, x, dev, stream)
     _launch(dev, stream, load().ramnet_norm_gate, R, D, groups, code, px, x.stride(0), pz, zs, pw, eps, bool(gate_first),
             y.data_ptr(), ycode)
     return y

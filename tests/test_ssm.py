@@ -463,6 +463,34 @@ def test_two_calls_at_once_on_streams_of_their_own():
     assert torch.equal(c[0], cref[0]) and torch.equal(c[1], cref[1]) and torch.equal(n, nref)
 
 
+def test_a_call_on_another_stream_leaves_memory_in_use_alone():
+    """Memory that was let go on the current stream, while work there still reads it, is not taken by a call that
+    runs on another stream."""
+    B, T, H, N, P = 2, 256, 4, 64, 64
+    cfg = ramnet.SsmConfig(H=H, G=1, N=N, P=P)
+    L = _layer(B, T, H, 1, N, P, BF)
+    flat = L["x"].flatten(2).contiguous()
+    w = torch.ones((H * P, 4), device="cuda")
+    ref = ramnet.ssm_forward(cfg, **L)
+    other = torch.cuda.Stream()
+    sizes = (ramnet.ssm_workspace_bytes(cfg, B, T), B * T * H * P * 2, B * H * N * P * 4, B * 3 * H * P * 2)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = [torch.full((n,), 77, dtype=torch.uint8, device="cuda") for n in sizes]
+    copies = [torch.empty_like(t) for t in held]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    for c, t in zip(copies, held):
+        c.copy_(t)
+    del held, t
+    y, S = ramnet.ssm_forward(cfg, **L, stream=other)
+    ramnet.conv_forward(flat, w, stream=other)
+    ramnet.norm_gate(flat.flatten(0, 1), stream=other.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(bool((c == 77).all()) for c in copies)
+    assert torch.equal(y, ref[0]) and torch.equal(S, ref[1])
+
+
 def test_steps_captured_and_replayed():
     """A layer's step (convolution, scan, norm) as one graph over fixed buffers, replayed on new tokens."""
     B, H, G, N, P, W = 3, 4, 2, 64, 64, 4
