@@ -103,14 +103,22 @@ __global__ void __launch_bounds__(256) k_ssm_decay(const SsmParams p, int chunks
     const float bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
     const double A = static_cast<double>(p.A[h]) * 1.4426950408889634074;
     float d[2];
+    double l[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int t = t0 + 2 * lane + k;
-        d[k] = 0.0f;  // a token that is not there neither decays nor writes
-        if (t < len) d[k] = step_size(load_in(p.dt, static_cast<size_t>(b * p.dts.b + t * p.dts.t + h * p.dts.h), 1), bias, p.softplus, p.dt_min, p.dt_max);
+        d[k] = 0.0f, l[k] = 0.0;  // a token that is not there neither decays nor writes
+        if (t < len) {
+            d[k] = step_size(load_in(p.dt, static_cast<size_t>(b * p.dts.b + t * p.dts.t + h * p.dts.h), 1), bias, p.softplus, p.dt_min, p.dt_max);
+            // 2^-1024 leaves nothing of any fp32 state: what decays further is taken as that much, so that sums of 64 tokens
+            // stay well within what `hi` and `lo` hold (past 3.4e38 their sum is no number; at 1e12 it is off by 4e-3).
+            // What is no number stays none.
+            l[k] = d[k] * A;
+            if (l[k] == l[k]) l[k] = fmin(fmax(l[k], -1024.0), 1024.0);
+        }
     }
-    const double a1 = d[1] * A;
-    double sum = d[0] * A + a1;
+    const double a1 = l[1];
+    double sum = l[0] + a1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const double up = __shfl_up_sync(0xffffffffu, sum, o);

@@ -1,0 +1,97 @@
+"""State space layer on the GPU at the edges of its definition, against the plain 64-bit form in oracle/ssm.py or a closed
+form.  Tolerances are those of test_ssm.py: the oracle's bound on fp32 roundings, 2^-15 of the sum of absolute values where
+bf16 prompts meet the state and the token-to-token weights as two bf16 pieces, half a step of the output's type."""
+import pytest
+import torch
+
+from oracle import ssm as plain
+from sparse_slot_recurrent_b200 import ramnet
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+U32 = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    ramnet.load()
+    yield
+    ramnet.sync_status()
+
+
+def _within(got, want, tol):
+    got = got.detach().cpu().double()
+    assert got.shape == want.shape and bool(torch.isfinite(got).all())
+    over = (got - want).abs() - tol
+    assert float(over.max()) <= 0, f"off by up to {float((got - want).abs().max()):.3g}, {float(over.max()):.3g} over the bound"
+
+
+def _operands(B, T, H, G, N, P, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    return dict(x=r(B, T, H, P).to(dtype).cuda(), dt=r(B, T, H).mul(0.5).to(dtype).cuda(), A=-(1 + 15 * torch.rand((H,), generator=g)).cuda(),
+                Bm=r(B, T, G, N).to(dtype).cuda(), Cm=r(B, T, G, N).to(dtype).cuda(), D=(torch.rand((H,), generator=g) + 0.5).cuda())
+
+
+def _token(L, t):
+    return {k: (v[:, t] if v is not None and v.dim() > 1 else v) for k, v in L.items()}
+
+
+def _check(cfg, L, S_in=None, lengths=None, **kw):
+    y, S = ramnet.ssm_forward(cfg, **L, S_in=S_in, lengths=lengths, **kw)
+    ramnet.sync_status()
+    wy, wS, ya, ye, E = plain.scan(**L, S_in=S_in, lengths=lengths, softplus=cfg.dt_softplus, dt_min=cfg.dt_min, dt_max=cfg.dt_max)
+    pieces = L["x"].dtype == BF and y.dtype == BF
+    ty = ye + wy.abs() * torch.finfo(y.dtype).eps / 2 + torch.finfo(y.dtype).tiny + (2.0 ** -15 * ya if pieces else 0)
+    # sums of 64 tokens at once: 64 more roundings than token by token
+    tS = E + (64 * U32 * wS.abs().amax(dim=(2, 3), keepdim=True) if pieces else 0) + 1e-30
+    for b in range(y.shape[0]):
+        n = y.shape[1] if lengths is None else min(max(int(lengths[b]), 0), y.shape[1])
+        if n:
+            _within(y[b, :n], wy[b, :n], ty[b, :n])
+    _within(S, wS, tS)
+    return y, S
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [70, 1100], ids=["whole", "cut"])
+def test_a_state_that_forgets_everything_at_every_token(dtype, T):
+    """d A from -1e30 to below fp32's lowest number, over a chunk and from one token on: the decay is 0, so that a token
+    sees itself alone, in the prompt as in single tokens."""
+    B, H, N, P = 1, 4, 64, 64
+    cfg = ramnet.SsmConfig(H=H, G=1, N=N, P=P)
+    L = _operands(B, T, H, 1, N, P, dtype)
+    L["A"] = torch.tensor([-1e32, -1e37, torch.finfo(F32).min, -float("inf")], device="cuda")
+    S_in = torch.randn((B, H, N, P), generator=torch.Generator().manual_seed(3)).cuda()
+    y, S = ramnet.ssm_forward(cfg, **L, S_in=S_in)
+    ramnet.sync_status()
+    x, Bm, Cm = (L[k].cpu().double() for k in ("x", "Bm", "Cm"))
+    d = plain.step_sizes(L["dt"], None)
+    g = (Bm * Cm).sum(-1)  # [B,T,1]
+    skip = L["D"].cpu().double()[:, None] * x
+    wy = (d * g)[..., None] * x + skip
+    ya = (d * (Bm * Cm).abs().sum(-1))[..., None] * x.abs() + skip.abs()
+    wS = d[:, -1, :, None, None] * Bm[:, -1, 0, None, :, None] * x[:, -1, :, None, :]
+    # a step size good to 16 u, then products and a sum over n
+    u = U32 * (N + 24)
+    _within(y, wy, ya * (u + (2.0 ** -15 if dtype == BF else 0)) + wy.abs() * torch.finfo(dtype).eps / 2 + 1e-30)
+    _within(S, wS, wS.abs() * U32 * 24 + 1e-30)
+    one = S_in.clone()
+    _within(ramnet.ssm_step(cfg, **_token(L, 5), S=one), wy[:, 5], ya[:, 5] * u + wy[:, 5].abs() * torch.finfo(dtype).eps / 2 + 1e-30)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_a_token_that_resets_the_state_leaves_its_chunk_precise(dtype):
+    """Slow decay but for a few tokens with d A = -1e12: what follows them in the same chunk decays by their own step sizes."""
+    B, T, H, N, P = 2, 150, 2, 64, 64
+    cfg = ramnet.SsmConfig(H=H, G=1, N=N, P=P, dt_softplus=False)
+    L = _operands(B, T, H, 1, N, P, dtype)
+    L["A"] = torch.tensor([-1e12, -3e12], device="cuda")
+    L["dt"] = (torch.rand((B, T, H), generator=torch.Generator().manual_seed(1)) * 1e-13 + 1e-14).to(dtype).cuda()
+    for t in (0, 20, 37, 64, 127):
+        L["dt"][:, t] = 1.0
+    L["D"] = None
+    _check(cfg, L)
