@@ -117,13 +117,14 @@ __global__ void __launch_bounds__(256) k_ssm_decay(const SsmParams p, int chunks
             if (l[k] == l[k]) l[k] = fmin(fmax(l[k], -1024.0), 1024.0);
         }
     }
-    const double a1 = l[1];
-    double sum = l[0] + a1;
+    double sum = l[0] + l[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const double up = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += up;
     }
+    double before = __shfl_up_sync(0xffffffffu, sum, 1);  // up to this lane's tokens, without them: its second may be no number
+    if (lane == 0) before = 0.0;
     const double total = __shfl_sync(0xffffffffu, sum, 31);
     const double blk_end = __shfl_sync(0xffffffffu, sum, lane | 7);
     double blk_start = __shfl_sync(0xffffffffu, sum, ((lane & 24) - 1) & 31);
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(256) k_ssm_decay(const SsmParams p, int chunks
     float hi[2], lo[2], e[2], w[2], u[2], v[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const double cum = k ? sum : sum - a1;
+        const double cum = k ? sum : before + l[0];
         hi[k] = static_cast<float>(cum);
         lo[k] = static_cast<float>(cum - static_cast<double>(hi[k]));
         e[k] = exp2f(hi[k]);

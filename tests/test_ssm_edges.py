@@ -95,3 +95,72 @@ def test_a_token_that_resets_the_state_leaves_its_chunk_precise(dtype):
         L["dt"][:, t] = 1.0
     L["D"] = None
     _check(cfg, L)
+
+
+CAUSAL = [
+    # T, H, G, N, P
+    (100, 4, 2, 64, 64),
+    (150, 3, 1, 128, 128),
+    (90, 5, 1, 16, 32),
+    (70, 2, 1, 32, 256),
+    (900, 2, 1, 64, 64),  # in segments
+    (40, 2, 1, 64, 16),
+]
+
+
+@pytest.mark.parametrize("shape", CAUSAL, ids=str)
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("what", ["Bm", "Cm", "dt"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
+def test_what_is_no_number_reaches_no_earlier_token(shape, dtype, what, bad):
+    T, H, G, N, P = shape
+    B, at = 2, T - 27
+    cfg = ramnet.SsmConfig(H=H, G=G, N=N, P=P)
+    L = _operands(B, T, H, G, N, P, dtype)
+    y0, S0 = ramnet.ssm_forward(cfg, **L)
+    M = dict(L, **{what: L[what].clone()})
+    hit = torch.zeros((B, H, P), dtype=torch.bool, device="cuda")  # what the value may reach, from its token on
+    if what == "x":
+        M["x"][1, at, H - 1, 5] = bad
+        hit[1, H - 1, 5] = True
+    elif what == "dt":
+        M["dt"][1, at, H - 1] = bad
+        hit[1, H - 1] = True
+    else:
+        M[what][1, at, G - 1, 3] = bad
+        hit[1, H - H // G:] = True
+    y, S = ramnet.ssm_forward(cfg, **M)
+    ramnet.sync_status()
+    assert torch.equal(y[:, :at], y0[:, :at])
+    keep = ~hit[:, None].expand(y.shape)
+    assert torch.equal(y[keep], y0[keep])
+    keepS = ~hit[:, :, None].expand(S.shape)
+    assert torch.equal(S[keepS], S0[keepS])
+    if what == "Cm":  # a token's C reaches that token's output alone
+        assert torch.equal(S, S0)
+        assert not bool(torch.isfinite(y[:, at][hit]).any())
+        after = torch.ones_like(y, dtype=torch.bool)
+        after[:, at] = False
+        assert torch.equal(y[after], y0[after])
+    else:
+        assert not bool(torch.isfinite(y[:, at:][hit[:, None].expand(y[:, at:].shape)]).any()) or what == "dt"
+        assert not bool(torch.isfinite(S.movedim(2, 3)[hit]).all(-1).any())
+
+
+@pytest.mark.parametrize("what", ["Bm", "Cm", "dt"])
+def test_numbers_that_are_none_in_a_ragged_batch(what):
+    """... in the last token of each of some sequences that end within a chunk; rows behind them stay as they were."""
+    B, T, H, G, N, P = 4, 200, 4, 2, 64, 64
+    cfg = ramnet.SsmConfig(H=H, G=G, N=N, P=P)
+    L = _operands(B, T, H, G, N, P, BF)
+    n = (1, 64, 97, 200)
+    lengths = torch.tensor(n, dtype=torch.int32).cuda()
+    y0, _ = ramnet.ssm_forward(cfg, **L, lengths=lengths, y=torch.full((B, T, H, P), 7.0, dtype=BF, device="cuda"))
+    for b in range(B):
+        L[what][b, n[b] - 1] = float("nan")
+    y, S = ramnet.ssm_forward(cfg, **L, lengths=lengths, y=torch.full((B, T, H, P), 7.0, dtype=BF, device="cuda"))
+    for b in range(B):
+        assert torch.equal(y[b, :n[b] - 1], y0[b, :n[b] - 1])
+        assert bool(torch.isnan(y[b, n[b] - 1]).all())
+        assert bool((y[b, n[b]:] == 7.0).all())
+        assert bool(torch.isnan(S[b]).all()) == (what != "Cm")
