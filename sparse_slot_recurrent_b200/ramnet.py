@@ -39,6 +39,17 @@ class RamnetError(RuntimeError):
         self.status = status
 
 
+_MAX = 2 ** 31 - 1
+
+
+def _fits(**sizes):
+    """Raises for a size that the library's 32-bit arguments do not hold (ctypes would cut it to its low bits, and the
+    library would see a small size that passes its checks)."""
+    for name, v in sizes.items():
+        if not -_MAX <= v <= _MAX:
+            raise RamnetError(RAMNET_ERR_INVALID_ARG, f"{name}={v} too large (32 bits)")
+
+
 class _Strides(ctypes.Structure):
     _fields_ = [("b", ctypes.c_int64), ("t", ctypes.c_int64), ("h", ctypes.c_int64)]
 
@@ -58,6 +69,9 @@ class Config:
     eps_gsu: float = 1e-6
     eps_norm: float = 1e-6
     renorm: int = 1
+
+    def __post_init__(self):
+        _fits(d_p=self.d_p, U=self.U, K=self.K, d_v=self.d_v, renorm=self.renorm)
 
     @property
     def M(self) -> int:
@@ -89,6 +103,7 @@ class SsmConfig:
     dt_max: float = float("inf")
 
     def __post_init__(self):
+        _fits(H=self.H, G=self.G, N=self.N, P=self.P)
         c = _SsmCfg(self.H, self.G, self.N, self.P, int(self.dt_softplus), self.dt_min, self.dt_max)
         object.__setattr__(self, "_ref", ctypes.pointer(c))
 
@@ -205,6 +220,7 @@ def decode_addresses(cfg: Config, logits: torch.Tensor, pos0=None, cape_mask=Non
     """logits [B,T,H,U*d_p] (fp32 or bf16; any strides with the last dimension contiguous)
     -> (idx int32 [B,T,H,K], w fp32 [B,T,H,K])."""
     B, T, H, L = logits.shape
+    _fits(B=B, T=T, H=H)
     if logits.stride(-1) != 1:
         raise ValueError("the last dimension of logits must be contiguous")
     _dense(pos0, cape_mask)
@@ -220,6 +236,7 @@ def decode_addresses(cfg: Config, logits: torch.Tensor, pos0=None, cape_mask=Non
 
 
 def scan_workspace_bytes(cfg: Config, B: int, T: int, H: int) -> int:
+    _fits(B=B, T=T, H=H)
     c = cfg._c()
     return int(load().ramnet_scan_workspace_bytes(ctypes.byref(c), B, T, H))
 
@@ -245,6 +262,7 @@ def scan_forward(cfg: Config, k_logits, q_logits, v, g, z, norm_w=None, cape_mas
                  m_in=None, out_dtype=torch.float32, y=None, S_out=None, m_out=None, workspace=None, stream=None):
     """Prefill scan.  Returns (y [B,T,H,d_v], S_out [B,H,M,d_v], m_out [B,H,M])."""
     B, T, H, L = k_logits.shape
+    _fits(B=B, T=T, H=H)
     dev = k_logits.device
     _dense(k_logits, q_logits, v, g, z, norm_w, cape_mask, pos0, S_in, m_in)
     if y is None:
@@ -265,6 +283,7 @@ def scan_forward(cfg: Config, k_logits, q_logits, v, g, z, norm_w=None, cape_mas
 
 
 def scan_forward_host_scratch_bytes(cfg: Config, B: int, T: int, H: int, in_dtype, out_dtype, pieces: int) -> int:
+    _fits(B=B, T=T, H=H, pieces=pieces)
     c = cfg._c()
     codes = {torch.bfloat16: RAMNET_BF16, torch.float32: RAMNET_F32}
     n = load().ramnet_scan_forward_host_scratch_bytes(ctypes.byref(c), B, T, H, codes[in_dtype], codes[out_dtype],
@@ -280,6 +299,7 @@ def scan_forward_host(cfg: Config, k_logits, q_logits, v, g, z, y, S_out, m_out,
     for overlap) and the rest on the device; run in ``pieces`` runs along T whose copies overlap
     the kernels.  ``scratch`` is a uint8 device tensor of scan_forward_host_scratch_bytes()."""
     B, T, H, L = k_logits.shape
+    _fits(B=B, T=T, H=H, pieces=pieces)
     for t in (k_logits, q_logits, v, g, z, y):
         if t.is_cuda or not t.is_contiguous():
             raise ValueError("host tensors must be contiguous CPU tensors")
@@ -296,6 +316,7 @@ def scan_route(cfg: Config, k_logits, q_logits, g, workspace, cape_mask=None, po
     """First launch of scan_forward: address decode, CAPE, write retentions, event grouping
     into ``workspace`` (uint8 device tensor of at least scan_workspace_bytes())."""
     B, T, H, L = k_logits.shape
+    _fits(B=B, T=T, H=H)
     _dense(k_logits, q_logits, g, cape_mask, pos0, workspace)
     c = cfg._c()
     _check(load().ramnet_scan_route(ctypes.byref(c), B, T, H, _dt(k_logits), _ptr(k_logits), _ptr(q_logits), _ptr(g),
@@ -306,6 +327,7 @@ def scan_route(cfg: Config, k_logits, q_logits, g, workspace, cape_mask=None, po
 def scan_recur(cfg: Config, v, z, y, S_out, m_out, workspace, norm_w=None, S_in=None, m_in=None, stream=None):
     """Second launch of scan_forward: the recurrence over the events scan_route wrote."""
     B, T, H, dv = v.shape
+    _fits(B=B, T=T, H=H)
     _dense(v, z, y, S_out, m_out, workspace, norm_w, S_in, m_in)
     c = cfg._c()
     _check(load().ramnet_scan_recur(ctypes.byref(c), B, T, H, _dt(v), _ptr(v), _ptr(z), _ptr(norm_w), _ptr(S_in),
@@ -319,6 +341,7 @@ def scan_forward_noalloc(cfg: Config, k_logits, q_logits, v, g, z, y, S_out, m_o
     """Prefill scan on the library's built-in scratch (no workspace argument).  All outputs
     are passed in; nothing is allocated.  Returns (y, S_out, m_out)."""
     B, T, H, L = k_logits.shape
+    _fits(B=B, T=T, H=H)
     _dense(k_logits, q_logits, v, g, z, norm_w, cape_mask, pos0, S_in, m_in, y, S_out, m_out)
     c = cfg._c()
     _check(load().ramnet_scan_forward_noalloc(
@@ -333,6 +356,7 @@ def decode_step(cfg: Config, k_logits, q_logits, v, g, z, S, m, pos=None, norm_w
     """One decode token per (b,h); S [B,H,M,d_v] and m [B,H,M] fp32 are updated in place.
     Returns y [B,H,d_v]."""
     B, H, L = k_logits.shape
+    _fits(B=B, H=H)
     _dense(k_logits, q_logits, v, g, z, S, m, pos, norm_w, cape_mask)
     if y is None:
         y = torch.empty((B, H, cfg.d_v), dtype=out_dtype, device=k_logits.device)
@@ -345,11 +369,13 @@ def decode_step(cfg: Config, k_logits, q_logits, v, g, z, S, m, pos=None, norm_w
 
 def selftest_wait_timeout(limit_us: int, stream=None):
     """Launch the failure-detection self-test (a bounded wait that must run out)."""
+    _fits(limit_us=limit_us)
     _check(load().ramnet_selftest_wait_timeout(limit_us, _stream(stream)))
 
 
 def set_scan_wait_limit(limit_us: int):
     """Limit of the prefill recurrence's bounded waits for later launches (0: 2 s default)."""
+    _fits(limit_us=limit_us)
     _check(load().ramnet_set_scan_wait_limit(limit_us))
 
 
@@ -444,6 +470,7 @@ def _launch(dev, stream, call, *args):
 
 
 def ssm_workspace_bytes(cfg: SsmConfig, B: int, T: int) -> int:
+    _fits(B=B, T=T)
     return int(load().ramnet_ssm_workspace_bytes(cfg._ref, B, T))
 
 
@@ -466,8 +493,10 @@ def ssm_forward(cfg: SsmConfig, x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=
     with the last dimension of x, Bm and Cm contiguous), A, D, dt_bias [H] fp32, lengths [B] int32.
     Returns (y [B,T,H,P] in out_dtype (x's if None), S_out [B,H,N,P] fp32).  Rows of a y that is passed in
     behind a sequence's last token keep their values; S_out may be S_in."""
-    code, dev, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
     B, T = x.shape[:2]
+    if B > _MAX or T > _MAX:
+        _fits(B=B, T=T)
+    code, dev, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
     state = (B, cfg.H, cfg.N, cfg.P)
     plen = _dense_ptr(lengths, "lengths", (B,), torch.int32, dev)
     pin = _dense_ptr(S_in, "S_in", state, torch.float32, dev)
@@ -488,8 +517,10 @@ def ssm_forward(cfg: SsmConfig, x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=
 def ssm_step(cfg: SsmConfig, x, dt, A, Bm, Cm, S, D=None, dt_bias=None, out_dtype=None, y=None, stream=None):
     """Selective scan for one token per sequence: x [B,H,P], dt [B,H], Bm and Cm [B,G,N]; S [B,H,N,P] fp32 is
     updated in place.  Returns y [B,H,P]."""
-    code, dev, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
     B = x.shape[0]
+    if B > _MAX:
+        _fits(B=B)
+    code, dev, (px, pdt, pA, pB, pC, pD, pbias) = _ssm_operands(cfg, x, dt, A, Bm, Cm, D, dt_bias)
     pS = _dense_ptr(S, "S", (B, cfg.H, cfg.N, cfg.P), torch.float32, dev)
     y, ycode = _output(y, "y", x.shape, out_dtype, x, dev, stream)
     (xb, xh, _), (db, dh), (bb, bg, _), (cb, cg, _) = x.stride(), dt.stride(), Bm.stride(), Cm.stride()
@@ -503,8 +534,10 @@ def conv_forward(x, w, bias=None, silu=True, lengths=None, state_in=None, out_dt
     """Short causal convolution over a prompt: x [B,T,C] (bf16 or fp32, channels contiguous), w [C,W] and
     bias [C] fp32, state_in [B,W-1,C] in x's dtype (the inputs before the first token; zeros if None).
     Returns (y [B,T,C], state_out [B,W-1,C]); state_out may be state_in."""
-    code, dev = _input(x, "x")
     (B, T, C), W, t, f32 = x.shape, w.shape[1], x.dtype, torch.float32
+    if B > _MAX or T > _MAX or C > _MAX or W > _MAX:
+        _fits(B=B, T=T, C=C, W=W)
+    code, dev = _input(x, "x")
     px, pw, pb = _rows_ptr(x, "x", x.shape, t, dev), _dense_ptr(w, "w", (C, W), f32, dev), _dense_ptr(bias, "bias", (C,), f32, dev)
     plen = _dense_ptr(lengths, "lengths", (B,), torch.int32, dev)
     pin = _dense_ptr(state_in, "state_in", (B, W - 1, C), t, dev)
@@ -520,8 +553,10 @@ def conv_forward(x, w, bias=None, silu=True, lengths=None, state_in=None, out_dt
 def conv_step(x, w, state, bias=None, silu=True, out_dtype=None, y=None, stream=None):
     """The convolution for one token per sequence: x [B,C]; state [B,W-1,C] in x's dtype takes the token in
     and drops its oldest.  Returns y [B,C]."""
-    code, dev = _input(x, "x")
     (B, C), W, t, f32 = x.shape, w.shape[1], x.dtype, torch.float32
+    if B > _MAX or C > _MAX or W > _MAX:
+        _fits(B=B, C=C, W=W)
+    code, dev = _input(x, "x")
     px, pw, pb = _rows_ptr(x, "x", x.shape, t, dev), _dense_ptr(w, "w", (C, W), f32, dev), _dense_ptr(bias, "bias", (C,), f32, dev)
     ps = _dense_ptr(state, "state", (B, W - 1, C), t, dev)
     y, ycode = _output(y, "y", x.shape, out_dtype, x, dev, stream)
@@ -532,8 +567,10 @@ def conv_step(x, w, state, bias=None, silu=True, out_dtype=None, y=None, stream=
 def norm_gate(x, z=None, w=None, groups=1, eps=1e-6, gate_first=True, out_dtype=None, y=None, stream=None):
     """RMSNorm of the rows of x [R,D] over ``groups`` groups of channels, times w [D] fp32, gated by silu(z)
     (z [R,D], None: no gate) before the norm or behind it.  Returns y [R,D]."""
-    code, dev = _input(x, "x")
     R, D = x.shape
+    if D > _MAX or not -_MAX <= groups <= _MAX:
+        _fits(D=D, groups=groups)
+    code, dev = _input(x, "x")
     px = _rows_ptr(x, "x", x.shape, x.dtype, dev)
     pz, zs = (None, 0) if z is None else (_rows_ptr(z, "z", x.shape, x.dtype, dev), z.stride(0))
     pw = _dense_ptr(w, "w", (D,), torch.float32, dev)

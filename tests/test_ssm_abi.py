@@ -135,3 +135,50 @@ def test_binding_checks_shapes_types_and_devices():
         ramnet.conv_step(torch.zeros(2, 8, **f), torch.zeros(8, 5, **f), torch.zeros(2, 4, 8, **f))
     with pytest.raises(ramnet.RamnetError):
         ramnet.norm_gate(torch.zeros(2, 8, **f), groups=3)
+
+
+# ------------------------------------------------------------------ sizes that the library's 32-bit arguments do not hold
+
+HUGE = (1 << 32) + 5  # 5 in 32 bits
+
+
+def _wide(*shape, dtype=torch.bfloat16):
+    return torch.zeros((1,) * len(shape), dtype=dtype).expand(shape)
+
+
+@pytest.mark.parametrize("name,call", [
+    ("T", lambda: ramnet.conv_forward(_wide(1, HUGE, 1), torch.zeros(1, 4))),
+    ("B", lambda: ramnet.conv_forward(_wide(HUGE, 1, 1), torch.zeros(1, 4))),
+    ("C", lambda: ramnet.conv_forward(_wide(1, 1, HUGE), _wide(HUGE, 4, dtype=torch.float32))),
+    ("W", lambda: ramnet.conv_forward(_wide(1, 3, 1), _wide(1, HUGE, dtype=torch.float32))),
+    ("B", lambda: ramnet.conv_step(_wide(HUGE, 1), torch.zeros(1, 4), _wide(HUGE, 3, 1))),
+    ("C", lambda: ramnet.conv_step(_wide(1, HUGE), _wide(HUGE, 4, dtype=torch.float32), _wide(1, 3, HUGE))),
+    ("W", lambda: ramnet.conv_step(_wide(1, 1), _wide(1, HUGE, dtype=torch.float32), _wide(1, HUGE - 1, 1))),
+    ("D", lambda: ramnet.norm_gate(_wide(1, HUGE))),
+    ("groups", lambda: ramnet.norm_gate(_wide(1, 5), groups=HUGE)),
+    ("groups", lambda: ramnet.norm_gate(_wide(1, 5), groups=1 - (1 << 32))),
+    ("T", lambda: ramnet.ssm_forward(_cfg(), _wide(1, HUGE, 4, 64), _wide(1, HUGE, 4), torch.zeros(4), _wide(1, HUGE, 2, 64), _wide(1, HUGE, 2, 64))),
+    ("B", lambda: ramnet.ssm_forward(_cfg(), _wide(HUGE, 2, 4, 64), _wide(HUGE, 2, 4), torch.zeros(4), _wide(HUGE, 2, 2, 64), _wide(HUGE, 2, 2, 64))),
+    ("B", lambda: ramnet.ssm_step(_cfg(), _wide(HUGE, 4, 64), _wide(HUGE, 4), torch.zeros(4), _wide(HUGE, 2, 64), _wide(HUGE, 2, 64),
+                                  _wide(HUGE, 4, 64, 64, dtype=torch.float32))),
+    ("T", lambda: ramnet.ssm_workspace_bytes(_cfg(), 1, (1 << 32) + 64)),
+    ("B", lambda: ramnet.ssm_workspace_bytes(_cfg(), HUGE, 64)),
+    ("H", lambda: _cfg(H=(1 << 32) + 4)),
+    ("N", lambda: _cfg(N=64 - (1 << 32))),
+    ("d_p", lambda: ramnet.Config(d_p=(1 << 32) + 4, U=2, K=4, d_v=64)),
+    ("K", lambda: ramnet.Config(d_p=4, U=2, K=(1 << 32) + 4, d_v=64)),
+    ("T", lambda: ramnet.scan_workspace_bytes(_SLOTS, 1, HUGE, 1)),
+    ("T", lambda: ramnet.decode_addresses(_SLOTS, _wide(1, HUGE, 1, 8), idx_out=torch.zeros(1), w_out=torch.zeros(1))),
+    ("T", lambda: ramnet.scan_forward_host_scratch_bytes(_SLOTS, 1, HUGE, 1, torch.bfloat16, torch.float32, 2)),
+    ("limit_us", lambda: ramnet.set_scan_wait_limit((1 << 32) + 5)),
+    ("limit_us", lambda: ramnet.selftest_wait_timeout((1 << 32) + 5)),
+], ids=lambda v: v if isinstance(v, str) else "")
+def test_sizes_past_32_bits_refused_by_the_binding(lib, name, call):
+    """... and not cut to their low 32 bits: the library would see a small size that passes its checks."""
+    with pytest.raises(ramnet.RamnetError, match=f"{name}=") as e:
+        call()
+    assert e.value.status == BAD
+    assert ramnet.set_scan_wait_limit(0) is None
+
+
+_SLOTS = ramnet.Config(d_p=4, U=2, K=4, d_v=64)
