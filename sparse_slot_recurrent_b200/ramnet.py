@@ -11,7 +11,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -106,6 +106,9 @@ class SsmConfig:
         _fits(H=self.H, G=self.G, N=self.N, P=self.P)
         c = _SsmCfg(self.H, self.G, self.N, self.P, int(self.dt_softplus), self.dt_min, self.dt_max)
         object.__setattr__(self, "_ref", ctypes.pointer(c))
+
+    def __reduce__(self):  # by its fields: the pointer is this object's own
+        return type(self), tuple(getattr(self, f.name) for f in fields(self))
 
 
 _lib = None

@@ -1,5 +1,9 @@
 """Host-side refusals of the state space layer's entry points, and of their Python binding (no GPU needed)."""
+import copy
 import ctypes
+import dataclasses
+import io
+import pickle
 
 import pytest
 import torch
@@ -182,3 +186,20 @@ def test_sizes_past_32_bits_refused_by_the_binding(lib, name, call):
 
 
 _SLOTS = ramnet.Config(d_p=4, U=2, K=4, d_v=64)
+
+
+@pytest.mark.parametrize("cfg", [ramnet.SsmConfig(H=6, G=3, N=32, P=128, dt_softplus=False, dt_min=0.001, dt_max=0.5),
+                                 ramnet.Config(d_p=4, U=2, K=4, d_v=64)], ids=["ssm", "slots"])
+def test_configurations_are_copied_and_pickled(lib, cfg):
+    """A layer that holds one is deep-copied, saved and sent to worker processes."""
+    for other in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg)), dataclasses.replace(cfg)):
+        assert other == cfg and hash(other) == hash(cfg) and repr(other) == repr(cfg)
+        if isinstance(cfg, ramnet.SsmConfig):
+            a, b = other._ref.contents, cfg._ref.contents
+            assert ctypes.addressof(a) != ctypes.addressof(b)
+            assert [getattr(a, f[0]) for f in a._fields_] == [getattr(b, f[0]) for f in b._fields_] == [6, 3, 32, 128, 0, b.dt_min, 0.5]
+            assert ramnet.ssm_workspace_bytes(other, 2, 100) == ramnet.ssm_workspace_bytes(cfg, 2, 100) > 0
+    saved = io.BytesIO()
+    torch.save({"cfg": cfg}, saved)
+    saved.seek(0)
+    assert torch.load(saved, weights_only=False)["cfg"] == cfg
