@@ -310,7 +310,7 @@ ramnet_status ramnet_decode_step(const ramnet_config* cfg, int32_t B, int32_t H,
 
 /* H heads of P channels with N state values per channel; head h uses the B and C vectors of
  * group h / (H/G).  Limits: P and N in {16, 32, 64, 128, 256}, G >= 1 divides H,
- * B*T*H < 2^31, B*H < 2^27, T <= 2^30. */
+ * B*T*H < 2^31, B*H < 2^27, T <= 2^30, for prompts H*P <= 2^30. */
 typedef struct {
     int32_t H, G, N, P;
     int32_t dt_softplus;   /* 1: step size softplus(dt + dt_bias), 0: dt + dt_bias          */

@@ -43,7 +43,8 @@ size_t elem(ramnet_dtype d) { return d == RAMNET_BF16 ? 2 : 4; }
     } while (0)
 #define MAY(p, n) CHECK((p) == nullptr || aligned(p, n), "%s not %zu-byte aligned", #p, (size_t)(n))
 
-// Longest sequence or row: indices may run a block past its end without leaving 32 bits.
+// Longest sequence or row, and most channels of a token of the scan: indices may run a block past the end without leaving
+// 32 bits.
 constexpr int64_t kLongest = 1ll << 30;
 
 bool side(int32_t n) { return n == 16 || n == 32 || n == 64 || n == 128 || n == 256; }
@@ -59,6 +60,14 @@ ramnet_status check_ssm(const ramnet_ssm_config* c, int64_t B, int64_t T)
     // (B*H first: the product of all three could pass 64 bits)
     CHECK(B * c->H <= (1ll << 27) - 1 && B * c->H * T <= (1ll << 31) - 1, "B*T*H too large");
     CHECK(T <= kLongest, "T too large");
+    return RAMNET_OK;
+}
+
+ramnet_status check_prompt(const ramnet_ssm_config* c, int64_t B, int64_t T)
+{
+    const ramnet_status st = check_ssm(c, B, T);
+    if (st != RAMNET_OK) return st;
+    CHECK(static_cast<int64_t>(c->H) * c->P <= kLongest, "H*P too large");
     return RAMNET_OK;
 }
 
@@ -104,7 +113,7 @@ extern "C" {
 size_t ramnet_ssm_workspace_bytes(const ramnet_ssm_config* cfg, int32_t B, int32_t T)
 {
     ramnet::set_last_error(RAMNET_OK, "");
-    if (check_ssm(cfg, B, T) != RAMNET_OK) return 0;
+    if (check_prompt(cfg, B, T) != RAMNET_OK) return 0;
     return ssm_workspace(cfg, B, T).total;
 }
 
@@ -116,7 +125,7 @@ ramnet_status ramnet_ssm_forward(const ramnet_ssm_config* cfg, int32_t B, int32_
                                  void* stream)
 {
     ramnet::set_last_error(RAMNET_OK, "");
-    const ramnet_status st = check_ssm(cfg, B, T);
+    const ramnet_status st = check_prompt(cfg, B, T);
     if (st != RAMNET_OK) return st;
     CHECK(valid_dtype(in_dt) && valid_dtype(out_dt), "bad dtype");
     ramnet::SsmParams p{};

@@ -203,3 +203,13 @@ def test_configurations_are_copied_and_pickled(lib, cfg):
     torch.save({"cfg": cfg}, saved)
     saved.seek(0)
     assert torch.load(saved, weights_only=False)["cfg"] == cfg
+
+
+@pytest.mark.parametrize("H,G,P", [((1 << 22) + 1, 1, 256), (1 << 23, 1 << 20, 256), ((1 << 26) + 3, 1, 16), (1 << 27, 2, 16)])
+def test_tokens_of_too_many_channels_refused(lib, H, G, P):
+    """Channels of a token are counted in 32 bits, up to a block past their end."""
+    cfg = _cfg(H=H, G=G, N=16, P=P)
+    assert _fwd(lib, cfg, B=1, T=1) == BAD
+    assert "large" in ramnet.last_error()
+    assert ramnet.ssm_workspace_bytes(cfg, 1, 1) == 0
+    assert ramnet.ssm_workspace_bytes(_cfg(H=(1 << 30) // P, G=1, N=16, P=P), 1, 1) > 0
