@@ -442,7 +442,8 @@ def _empty(shape, dtype, device, stream):
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        handle = _stream(stream)  # (an ExternalStream of handle 0 would be some new stream, not the default one)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 

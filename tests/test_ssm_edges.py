@@ -164,3 +164,43 @@ def test_numbers_that_are_none_in_a_ragged_batch(what):
         assert bool(torch.isnan(y[b, n[b] - 1]).all())
         assert bool((y[b, n[b]:] == 7.0).all())
         assert bool(torch.isnan(S[b]).all()) == (what != "Cm")
+
+
+def _owner(t):
+    """The stream whose memory a tensor lies in."""
+    at = t.data_ptr()
+    return [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"]]
+
+
+def test_memory_of_a_call_on_the_default_stream_by_its_handle():
+    """stream=0, while another stream is current: outputs and workspace lie in the default stream's memory."""
+    B, T, H, N, P = 2, 100, 4, 64, 64
+    cfg = ramnet.SsmConfig(H=H, G=1, N=N, P=P)
+    L = _operands(B, T, H, 1, N, P, BF)
+    flat, w = L["x"].flatten(2), torch.ones((H * P, 4), device="cuda")
+    ref = ramnet.ssm_forward(cfg, **L)
+    S = torch.zeros((B, H, N, P), device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        outs = [*ramnet.ssm_forward(cfg, **L, stream=0), ramnet.ssm_step(cfg, **_token(L, 0), S=S, stream=0),
+                *ramnet.conv_forward(flat, w, stream=0), ramnet.norm_gate(flat.flatten(0, 1), stream=torch.cuda.default_stream().cuda_stream)]
+        for t in outs:
+            assert _owner(t) == [0]
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], ref[0]) and torch.equal(outs[1], ref[1])
+
+
+def test_memory_of_a_call_on_a_stream_by_its_handle_or_as_an_object():
+    class Wrapped:  # what the slot layer's calls take as a stream too
+        def __init__(self, s):
+            self.cuda_stream = s.cuda_stream
+
+    s = torch.cuda.Stream()
+    x = torch.randn((5, 64), device="cuda")
+    want = ramnet.norm_gate(x)
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream, Wrapped(s)):
+        y = ramnet.norm_gate(x, stream=stream)
+        assert _owner(y) == [s.cuda_stream]
+        s.synchronize()
+        assert torch.equal(y, want)
