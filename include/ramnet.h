@@ -336,7 +336,8 @@ typedef struct {
  *   workspace  device scratch of ramnet_ssm_workspace_bytes() bytes, 16-byte aligned; not used
  *           by other work during the call, nor by a graph that may be replayed beside it
  * The state is fp32, and every sum has a fixed order: the same call gives the same bits.  Waits
- * on the device are bounded (2 s); one that runs out is reported by ramnet_sync_status.
+ * on the device are bounded (ramnet_set_scan_wait_limit); one that runs out is reported by
+ * ramnet_sync_status.
  * Errors: INVALID_ARG (sizes, NULL, negative strides, alignment, small workspace).
  */
 size_t ramnet_ssm_workspace_bytes(const ramnet_ssm_config* cfg, int32_t B, int32_t T);
@@ -410,12 +411,14 @@ ramnet_status ramnet_selftest_wait_timeout(uint32_t limit_us, void* stream);
 /*
  * ramnet_set_scan_wait_limit -- failure-detection hook, no counterpart in the pages.  Sets
  * the limit of every bounded wait inside the prefill recurrence (ramnet_scan_recur,
- * ramnet_scan_forward, ramnet_scan_forward_noalloc) launched after the call, for the whole
+ * ramnet_scan_forward, ramnet_scan_forward_noalloc) and the selective scan (ramnet_ssm_forward)
+ * launched after the call, for the whole
  * process: limit_us microseconds, or 0 for the default of 2 s.  A wait that runs out records
  * RAMNET_ERR_TIMEOUT in the device status word and the kernel winds down: its remaining
  * work is skipped, so y, S_out and m_out are then incomplete.  A limit far below the
  * kernel's own hand-over times makes the recurrence time out on purpose, which is how its
- * abort path is tested.
+ * abort path is tested.  The selective scan counts polls of 4 us; below that its waits give up
+ * at once.
  * Errors: INVALID_ARG if limit_us > 2000000.
  */
 ramnet_status ramnet_set_scan_wait_limit(uint32_t limit_us);

@@ -12,7 +12,7 @@
 namespace {
 
 thread_local std::string g_last_error;
-// limit of every bounded wait of the prefill recurrence (process-wide; ramnet_set_scan_wait_limit)
+// limit of every bounded wait of the prefill recurrence and of the selective scan (process-wide; ramnet_set_scan_wait_limit)
 std::atomic<uint64_t> g_scan_wait_ns{2000000000ull};
 
 // Device-side status word of this library (one per device that loads the library).
@@ -89,6 +89,7 @@ uint32_t* device_status_ptr()
 namespace ramnet {
 
 uint32_t* library_status_word() { return device_status_ptr(); }
+int scan_wait_ns() { return static_cast<int>(g_scan_wait_ns.load(std::memory_order_relaxed)); }
 
 // Sets the text ramnet_last_error returns on this thread (for entry points in other files).
 ramnet_status set_last_error(ramnet_status s, const char* msg)

@@ -67,6 +67,8 @@ struct ChunkTok {
     double total, pad;     // a_63
 };
 constexpr int kChunk = 64;
+constexpr int kWaitNs = 2000000000;  // default limit of a wait
+constexpr int kPollNs = 4000;        // a poll of a barrier that is not there yet, suspended by the hardware (measured)
 
 struct SsmParams {
     const void* x;  // [B,T,H,P]
@@ -94,6 +96,7 @@ struct SsmParams {
     float* seg_decay;  // [B,H,pieces]
     ChunkTok* toks;    // [B,H,ceil(T/64)], the tensor-core form only
     uint32_t* status;
+    int poll_cost;  // of a wait of the tensor-core form: what one poll takes of the kWaitNs that it may last
     int64_t chain_first;  // first (sequence, head) of a launch of the chaining kernel
 };
 
@@ -135,6 +138,8 @@ struct NormParams {
 
 // Device address of the library's status word on the current device (null on a CUDA error).
 uint32_t* library_status_word();
+// Limit of each wait of a prompt's kernels (ramnet_set_scan_wait_limit), at most kWaitNs.
+int scan_wait_ns();
 
 cudaError_t launch_conv(const ConvParams& p, cudaStream_t stream);
 cudaError_t launch_conv_step(const ConvStepParams& p, cudaStream_t stream);

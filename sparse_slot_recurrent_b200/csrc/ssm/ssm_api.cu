@@ -157,6 +157,8 @@ ramnet_status ramnet_ssm_forward(const ramnet_ssm_config* cfg, int32_t B, int32_
     p.lengths = lengths, p.S_in = S_in, p.y = y, p.S_out = S_out;
     p.B = B, p.T = T, p.H = cfg->H, p.G = cfg->G, p.N = cfg->N, p.P = cfg->P;
     p.softplus = cfg->dt_softplus != 0, p.dt_min = cfg->dt_min, p.dt_max = cfg->dt_max;
+    const int polls = ramnet::scan_wait_ns() / ramnet::kPollNs;  // of one wait
+    p.poll_cost = polls > 0 ? ramnet::kWaitNs / polls : ramnet::kWaitNs + 1;
     p.status = ramnet::library_status_word();
     if (p.status == nullptr) return launched(cudaGetLastError(), "status word");
     return launched(ramnet::launch_ssm_scan(p, static_cast<cudaStream_t>(stream)), "ssm_forward launch");

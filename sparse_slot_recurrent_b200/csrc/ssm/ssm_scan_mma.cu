@@ -176,12 +176,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     extern __shared__ unsigned char raw[];
     __shared__ __align__(8) uint64_t bar_mem[kBars];
     __shared__ uint32_t tmem_holder;
-    __shared__ int abort_mem;
+    __shared__ __align__(8) int limit_mem[2];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t s0 = smem_addr(sm), bars = smem_addr(bar_mem);
     ChunkTok* toks = reinterpret_cast<ChunkTok*>(sm + L.tok_off);
-    volatile int* abort_flag = &abort_mem;
-    const uint32_t abort_addr = smem_addr(&abort_mem);
+    volatile int* abort_flag = limit_mem;
+    const uint32_t limit_addr = smem_addr(limit_mem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // which channels and tokens
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     const int head0 = c0 / P;                          // first head, within the group
 
     auto bar = [&](int i) { return bars + 8u * i; };
-    auto wait = [&](int i, uint32_t parity) { wait_phase(bars + 8u * i, parity, abort_addr); };
+    auto wait = [&](int i, uint32_t parity) { wait_phase(bars + 8u * i, parity, limit_addr); };
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kBars; ++i) {
@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             if (i == kDsFree || i == kDsFree + 1) count = kOutWarps / HALVES;
             mbar_init(bar_mem + i, count);
         }
-        abort_mem = 0;
+        limit_mem[0] = p.poll_cost > kWaitNs;  // not even one: no wait waits, and the kernel gives up
+        limit_mem[1] = p.poll_cost;
         fence_mbar_init_cluster();
     }
     if (warp == kMmaWarp) tmem_alloc(&tmem_holder, 512);
@@ -306,12 +307,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         fence_async_smem();
         done(kOut + (c & 1));
     };
-    auto drain = [&](int i) {  // after an abort: tensor memory is given back only when nothing writes to it
-        if (*abort_flag && lane == 0) {
-            const uint64_t t_end = now_ns() + 2000000000ull;
+    // Before a block ends, whichever of its waits ran out and in whichever role: what was started has come to its end (bounded,
+    // and whatever the abort flag says).  No copy may land in its memory, and no product write to its tensor memory, after that.
+    auto over = [&](int i, uint32_t parity) {
+        const uint64_t t_end = now_ns() + 2000000000ull;
+        for (uint32_t it = 0; it < kSpinLimit; ++it)
+            if (try_wait(bar(i), parity) || now_ns() > t_end) break;
+    };
+    auto drain = [&](int i) {  // (a commit covers the products of the thread that makes it, the elected one that issued them)
+        if (elect_one()) {
             mma_commit(bar(i));
-            for (uint32_t it = 0; it < kSpinLimit; ++it)
-                if (try_wait(bar(i), 0) || now_ns() > t_end) break;
+            over(i, 0);
         }
         __syncwarp();
     };
@@ -566,13 +572,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             }
         }
         if (OUT && lane < 4) store_done();
-        // no copy may land in this block's memory after it has gone (bounded, also after an abort)
-        if (*abort_flag && lane == 0) {
-            const uint64_t t_end = now_ns() + 2000000000ull;
-            for (int c = issued > L.stages ? issued - L.stages : 0; c < issued; ++c)
-                for (uint32_t it = 0; it < kSpinLimit; ++it)
-                    if (try_wait(bar(kLanded + c % L.stages), (c / L.stages) & 1) || now_ns() > t_end) break;
-        }
+        if (lane == 0)
+            for (int c = issued > L.stages ? issued - L.stages : 0; c < issued; ++c) over(kLanded + c % L.stages, (c / L.stages) & 1);
+        __syncwarp();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------ MMA issue: G and dS (whole warp, one lane issues)
         regs_down<kMiscRegs>();

@@ -1,6 +1,8 @@
 """State space layer on the GPU at the edges of its definition, against the plain 64-bit form in oracle/ssm.py or a closed
 form.  Tolerances are those of test_ssm.py: the oracle's bound on fp32 roundings, 2^-15 of the sum of absolute values where
 bf16 prompts meet the state and the token-to-token weights as two bf16 pieces, half a step of the output's type."""
+import time
+
 import pytest
 import torch
 
@@ -204,3 +206,50 @@ def test_memory_of_a_call_on_a_stream_by_its_handle_or_as_an_object():
         assert _owner(y) == [s.cuda_stream]
         s.synchronize()
         assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("shape", [(4, 2048, 16, 128, 128), (2, 300, 4, 64, 64), (2, 1500, 6, 32, 16), (3, 130, 5, 128, 32),
+                                   (8, 256, 32, 32, 128)], ids=str)
+def test_waits_that_run_out_are_reported_and_the_context_survives(shape):
+    """A prompt on the tensor cores with limits on its waits that its hand-overs outlast (on purpose; nothing is lost on the
+    device).  Below 4 us every wait gives up at once; at one to three polls of 4 us those do that take longer, with copies and
+    products in flight, or none.  The kernels end by themselves, with RAMNET_ERR_TIMEOUT recorded if any gave up and the
+    usual bits if none did; nothing outside the outputs is written, and a call with the default limit then gives its usual bits."""
+    B, T, H, P, N = shape
+    cfg = ramnet.SsmConfig(H=H, G=1, N=N, P=P)
+    L = _operands(B, T, H, 1, N, P, BF)
+    lengths = torch.tensor(([T, T - 37, 70, T] * 2)[:B], dtype=torch.int32).cuda()
+    y0, S0 = (torch.full((B, T, H, P), 5.0, dtype=BF, device="cuda"), torch.zeros((B, H, N, P), device="cuda"))
+    ramnet.ssm_forward(cfg, **L, lengths=lengths, y=y0, S_out=S0)
+    ramnet.sync_status()
+    guard = torch.full((3, B, T, H, P), 5.0, dtype=BF, device="cuda")  # y lies between values that are nobody's to write
+    other = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for limit in (1, 3, 4, 8, 12, 4, 1):
+        other.zero_()  # inputs come from memory, not from L2
+        guard[1] = 5.0
+        t0 = time.perf_counter()
+        ramnet.set_scan_wait_limit(limit)
+        try:
+            _, S = ramnet.ssm_forward(cfg, **L, lengths=lengths, y=guard[1])
+            if limit < 4:
+                with pytest.raises(ramnet.RamnetError) as e:
+                    ramnet.sync_status()
+                assert e.value.status == ramnet.RAMNET_ERR_TIMEOUT
+            else:
+                try:
+                    ramnet.sync_status()
+                    assert torch.equal(guard[1], y0) and torch.equal(S, S0)
+                except ramnet.RamnetError as e:
+                    assert e.status == ramnet.RAMNET_ERR_TIMEOUT
+                    print("gave up at", limit, "us")
+        finally:
+            ramnet.set_scan_wait_limit(0)
+        assert time.perf_counter() - t0 < 5.0
+        ramnet.sync_status()  # cleared
+        assert bool((guard[0] == 5.0).all()) and bool((guard[2] == 5.0).all())
+        for b in range(B):
+            assert bool((guard[1, b, int(lengths[b]):] == 5.0).all())
+        y, S = torch.full_like(y0, 5.0), torch.zeros_like(S0)
+        ramnet.ssm_forward(cfg, **L, lengths=lengths, y=y, S_out=S)
+        ramnet.sync_status()
+        assert torch.equal(y, y0) and torch.equal(S, S0)
