@@ -303,9 +303,9 @@ ramnet_status ramnet_decode_step(const ramnet_config* cfg, int32_t B, int32_t H,
  * been projected.  Shapes name contiguous last dimensions; per-token inputs take element
  * strides (as ramnet_strides) and need only element alignment, so slices of one wide
  * projection are read in place.  Outputs share no memory with inputs, but for states where that
- * is said, and state arrays start on 16 bytes, as y does.  Non-finite inputs spread within their head or row (in
- * ramnet_ssm_forward also to the up to 63 tokens before them); tokens that a sequence does not
- * have (see `lengths`) may hold anything.
+ * is said, and state arrays start on 16 bytes, as y does.  Non-finite inputs spread within their
+ * head or row, and to no token before their own; tokens that a sequence does not have (see
+ * `lengths`) may hold anything.
  */
 
 /* H heads of P channels with N state values per channel; head h uses the B and C vectors of

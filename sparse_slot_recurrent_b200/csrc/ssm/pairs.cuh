@@ -57,6 +57,8 @@ __device__ __forceinline__ uint32_t pack_cut(F2 p)  // the leading 8 bits of bot
     un(p, a, b);
     return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
+// Adds the products of a pair of bf16 with 0: a sum of these stays +-0 unless one of the values is no number.
+__device__ __forceinline__ void add_zeros(uint32_t& sum, uint32_t pair) { asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(pair), "r"(0)); }
 // The leading 8 bits of both as one pair of bf16; p keeps what is left, negated (exact).  The differences take the
 // bf16 halves as they are, on the multiply-add pipe: the integer pipe has enough to do (a split that masks and
 // subtracts in 32 bits measured 7.4 issue cycles per pair, this one 4.8).

@@ -28,6 +28,10 @@
 // The loops over chunks chain W -> Ya, Yb -> outputs and state -> Yb; the rest overlaps.  Launches follow one another as
 // programmatic dependents.
 //
+// What is no number spreads forward in time only.  B, C and step sizes meet other tokens through W alone, whose upper triangle
+// is selected, not multiplied; but x_j meets every W[i,j] of its chunk in Ya, and 0 NaN is NaN.  So x that is no number is
+// taken as 0, and its channel's outputs and final state from that token on are set to NaN.
+//
 // The code of all roles has to stay within the instruction cache: with the loops fully unrolled (72 KB) every role
 // waited for instructions and a prompt took a third longer; unrolling W alone costs 3%.
 // Measured, B4 T16384 H16 P128 N128: 315 us (574 MB: 87 us at the copy bandwidth; token by token in registers 14 ms).
@@ -35,6 +39,8 @@
 // operand warps of the first quadrant, whose diagonal and off-diagonal blocks of W take 1300 cycles of issue and latency
 // between a chunk's G and its Ya.
 // B8 T4096 H8 P128 N128: 95 us with 2 segments per sequence; B6 T1021 H24 P64 N64 in 2 groups: 37 us.
+#include <climits>
+
 #include "ssm_mma.cuh"
 
 namespace ramnet {
@@ -177,11 +183,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     __shared__ __align__(8) uint64_t bar_mem[kBars];
     __shared__ uint32_t tmem_holder;
     __shared__ __align__(8) int limit_mem[2];
+    __shared__ int first_bad[128], any_bad_mem;  // per channel, its first token whose x is no number; whether there is one
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t s0 = smem_addr(sm), bars = smem_addr(bar_mem);
     ChunkTok* toks = reinterpret_cast<ChunkTok*>(sm + L.tok_off);
     volatile int* abort_flag = limit_mem;
     const uint32_t limit_addr = smem_addr(limit_mem);
+    volatile int* any_bad = &any_bad_mem;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // which channels and tokens
@@ -208,8 +216,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
         }
         limit_mem[0] = p.poll_cost > kWaitNs;  // not even one: no wait waits, and the kernel gives up
         limit_mem[1] = p.poll_cost;
+        any_bad_mem = 0;
         fence_mbar_init_cluster();
     }
+    if (OUT && threadIdx.x < 128) first_bad[threadIdx.x] = INT_MAX;
     if (warp == kMmaWarp) tmem_alloc(&tmem_holder, 512);
     if (OUT) {  // the blocks of W above its diagonal stay zero
         uint4* w = reinterpret_cast<uint4*>(sm + L.w_off);
@@ -396,6 +406,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     }
                 }
                 fence_async_smem();
+                uint32_t sum[2] = {0, 0};  // (here, since the loads of x have long ended: 3% less than in front of W)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) add_zeros(sum[k & 1], x[k >> 3][(k >> 2) & 1][k & 3]);
+                if (__any_sync(0xffffffffu, ((sum[0] | sum[1]) & 0x7fff7fffu) != 0)) {
+                    // In this warp's 32 channels and 32 tokens, which no other reads: zeros in place of what is no number.
+                    const int ch = q * 32 + lane, t0 = part * 32;
+                    int first = INT_MAX;
+#pragma unroll 1
+                    for (int t = t0 + 31; t >= t0; --t) {
+                        uint16_t* at = reinterpret_cast<uint16_t*>(sm + st * L.stage_bytes + (ch >> 6) * 8192 + t * 128 + ((((ch & 63) >> 3) ^ (t & 7)) << 4) + (ch & 7) * 2);
+                        if ((*at & 0x7f80) == 0x7f80) *at = 0, first = r.first + c * kQ + t;
+                    }
+                    if (first != INT_MAX) atomicMin(first_bad + ch, first);
+                    *any_bad = 1;
+                    __syncwarp();
+#pragma unroll
+                    for (int tg = 0; tg < 2; ++tg) fetch(st, part * 2 + tg, x[tg]);
+                }
                 if (NBUF == 2) read();
                 tmem_fence_after_sync();
 #pragma unroll
@@ -515,6 +543,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             if (!OUT) to = p.seg_state + (bh * p.split.slots() + seg) * np + own;
             else if (seg == p.split.nseg - 1) to = p.S_out + bh * np + own;
         }
+        if (OUT && to && first_bad[q * 32 + lane] != INT_MAX) {
+            const float none = __int_as_float(0x7fffffff);
+#pragma unroll
+            for (int k = 0; k < NC / 2; ++k) S[k] = f2(none, none);
+        }
         if (to) {
 #pragma unroll
             for (int k = 0; k < NC / 2; ++k) un(S[k], to[2 * k * P], to[(2 * k + 1) * P]);
@@ -572,6 +605,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
             }
         }
         if (OUT && lane < 4) store_done();
+        if (OUT && *any_bad) {
+            __syncwarp();
+            // all outputs are there: none of a channel from its first x that is no number on
+            for (int k = 0; k < 128; ++k) {
+                if (c0 + k >= cend) break;
+                for (int64_t t = static_cast<int64_t>(first_bad[k]) + lane; t < r.last; t += 32)
+                    reinterpret_cast<uint16_t*>(p.y)[((static_cast<int64_t>(b) * p.T + t) * p.H + g * hg) * P + c0 + k] = 0x7fff;
+            }
+        }
         if (lane == 0)
             for (int c = issued > L.stages ? issued - L.stages : 0; c < issued; ++c) over(kLanded + c % L.stages, (c / L.stages) & 1);
         __syncwarp();

@@ -112,7 +112,7 @@ CAUSAL = [
 
 @pytest.mark.parametrize("shape", CAUSAL, ids=str)
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
-@pytest.mark.parametrize("what", ["Bm", "Cm", "dt"])
+@pytest.mark.parametrize("what", ["x", "Bm", "Cm", "dt"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=["nan", "inf"])
 def test_what_is_no_number_reaches_no_earlier_token(shape, dtype, what, bad):
     T, H, G, N, P = shape
@@ -149,7 +149,7 @@ def test_what_is_no_number_reaches_no_earlier_token(shape, dtype, what, bad):
         assert not bool(torch.isfinite(S.movedim(2, 3)[hit]).all(-1).any())
 
 
-@pytest.mark.parametrize("what", ["Bm", "Cm", "dt"])
+@pytest.mark.parametrize("what", ["x", "Bm", "Cm", "dt"])
 def test_numbers_that_are_none_in_a_ragged_batch(what):
     """... in the last token of each of some sequences that end within a chunk; rows behind them stay as they were."""
     B, T, H, G, N, P = 4, 200, 4, 2, 64, 64
