@@ -3,11 +3,14 @@ token by token on the CPU, and how far a 32-bit evaluation may be from it.
 
 It shares no code with the CUDA path.  ``scan`` also returns bounds on the error of y and S that follow
 from the roundings of one token's update: with u = 2^-24 (half a step of fp32),
-  - d = softplus(dt + bias): the sum, exp and log1p are each off by a few u: taken as 8 u d;
-  - a = exp(d A): 8 u |d A| from d and 1 u |d A| from the product, 2 u of the exp: (2 + 9 |d A|) u a;
+  - d = softplus(v), v = dt + bias: rounding v moves d by up to u |v| softplus'(v) = u |v| sigmoid(v) (for v far below zero,
+    where softplus is the exponential, that is |v| u of d itself), and max, exp, log1p and the sum after them are each off
+    by a few u: e = u (|v| sigmoid(v) + 8 d); without the softplus u |v|; where a limit is taken instead, u of that
+    limit, which is a 32-bit number;
+  - a = exp(d A): |A| e from d and u |d A| from the product, 2 u of the exp: (|A| e + u (2 + |d A|)) a;
   - S' = a S + (d B) x: three more roundings of products and one of the sum.
-So E' = a E + u ((4 + 9 |d A|) a |S| + 12 d |B||x| + |S'|) bounds the state's error, where |S| is the state
-made of absolute values; y adds |C| E, N + 2 roundings of the sum over n, and 2 of D x.
+So E' = a E + (|A| e + u (4 + |d A|)) a |S| + (e + 4 u d) |B||x| + u |S'| bounds the state's error, where |S| is the
+state made of absolute values; y adds |C| E, N + 2 roundings of the sum over n, and 2 of D x.
 """
 from __future__ import annotations
 
@@ -27,6 +30,18 @@ def step_sizes(dt, bias, softplus=True, lo=0.0, hi=float("inf")):
     return torch.clamp(v, lo, hi)
 
 
+def step_errors(dt, bias, softplus=True, lo=0.0, hi=float("inf")):
+    """The bound e of above on the error of a step size in 32 bits."""
+    v = _d(dt) + (0 if bias is None else _d(bias))
+    if softplus:
+        d = torch.clamp(v, min=0) + torch.log1p(torch.exp(-v.abs()))
+        e = U32 * (v.abs() * torch.sigmoid(v) + 8 * d)
+    else:
+        d, e = v, U32 * v.abs()
+    limited = torch.clamp(d, lo, hi)
+    return torch.where((d < lo - e) | (d > hi + e), U32 * limited.abs(), torch.maximum(e, U32 * limited.abs()))
+
+
 def scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=None, S_in=None, softplus=True, dt_min=0.0, dt_max=float("inf")):
     """y [B,T,H,P] (zeros behind a sequence), S [B,H,N,P], the sums of absolute values behind y, and the bounds
     (y, S) of the 32-bit errors described above."""
@@ -34,6 +49,7 @@ def scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=None, S_in=None, softpl
     B, T, H, P = x.shape
     G, N = Bm.shape[2:]
     d = step_sizes(dt, dt_bias, softplus, dt_min, dt_max)
+    e = step_errors(dt, dt_bias, softplus, dt_min, dt_max)
     D = torch.zeros(H, dtype=torch.float64) if D is None else _d(D)
     Bm, Cm = Bm.repeat_interleave(H // G, 2), Cm.repeat_interleave(H // G, 2)
     y, ya, ye = (torch.zeros((B, T, H, P), dtype=torch.float64) for _ in range(3))
@@ -44,8 +60,11 @@ def scan(x, dt, A, Bm, Cm, D=None, dt_bias=None, lengths=None, S_in=None, softpl
         for t in range(n):
             dA = (d[b, t] * A)[:, None, None]
             a = torch.exp(dA)
-            w = (d[b, t, :, None] * Bm[b, t])[:, :, None] * x[b, t, :, None, :]
-            E[b] = a * E[b] + U32 * ((4 + 9 * dA.abs()) * a * Sa[b] + 12 * w.abs())
+            bx = Bm[b, t][:, :, None] * x[b, t, :, None, :]
+            w, ed = d[b, t][:, None, None] * bx, e[b, t][:, None, None]
+            # (a decay of 0 has no error, however large |A|)
+            E[b] = a * E[b] + torch.where(a > 0, A.abs()[:, None, None] * ed + U32 * (4 + dA.abs()), 0.0) * a * Sa[b]
+            E[b] += (ed + 4 * U32 * d[b, t][:, None, None]) * bx.abs()
             S[b] = a * S[b] + w
             Sa[b] = a * Sa[b] + w.abs()
             E[b] += U32 * Sa[b]
