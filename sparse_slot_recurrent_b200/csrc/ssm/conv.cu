@@ -4,7 +4,7 @@
 // with the W-1 inputs before the first token taken from a carried state.  Sums in fp32.
 //
 // Bound: HBM, one read of x and one write of y (2 W flops per element).  A thread owns V
-// neighbouring channels (16 bytes, or what addresses allow) over a run of tokens and slides a
+// neighbouring channels (16 bytes, or two or one where addresses allow no more) over a run of tokens and slides a
 // window of W-1 inputs in registers, so each input is read once but for W-1 rows per run (which
 // the run before has just brought into L2).  Rows come through a ring in shared memory that
 // only its own thread fills and reads, up to fourteen in flight.  For 4 x 16384 x 2304 bf16 channels: 273 us with one
@@ -212,7 +212,7 @@ cudaError_t pick_v(const P& p, int v, cudaStream_t s)
 {
     if (p.in_bf16) {
         if (v == 8) return pick_out<W, 8, true>(p, s);
-        return v >= 2 ? pick_out<W, 2, true>(p, s) : pick_out<W, 1, true>(p, s);
+        return v == 2 ? pick_out<W, 2, true>(p, s) : pick_out<W, 1, true>(p, s);
     }
     if (v == 4) return pick_out<W, 4, false>(p, s);
     return v == 2 ? pick_out<W, 2, false>(p, s) : pick_out<W, 1, false>(p, s);

@@ -7,7 +7,8 @@
 // Bound: HBM, x and z read once and y written once.  k_norm_warp: one warp per group of one row,
 // with all of the group's loads in flight before the first is used and no barrier (groups up to
 // 256 vectors: 2048 bf16 or 1024 fp32 channels at 16 bytes).  k_norm_block: one block per group, for longer groups; what it
-// does not keep in registers it reads again, from L2.  Vectors are as wide as rows and addresses allow.
+// does not keep in registers it reads again, from L2.  Vectors of 16 bytes, or of two values or one where rows and
+// addresses allow no more.
 // (One block per row for all: 229 us for 65536 x 2048 bf16 rows, the block's barrier and its few
 // bytes in flight.)
 #include "rows.cuh"
@@ -189,7 +190,7 @@ cudaError_t launch_norm_gate(const NormParams& p, cudaStream_t s)
     const int v = widest(p.in_bf16, {p.D / p.groups, p.sx, p.z ? p.sz : 0}, {p.x, p.z});
     if (p.in_bf16) {
         if (v == 8) return pick<8, true>(p, s);
-        return v >= 2 ? pick<2, true>(p, s) : pick<1, true>(p, s);
+        return v == 2 ? pick<2, true>(p, s) : pick<1, true>(p, s);
     }
     if (v == 4) return pick<4, false>(p, s);
     return v == 2 ? pick<2, false>(p, s) : pick<1, false>(p, s);

@@ -78,7 +78,8 @@ struct Raw {
     }
 };
 
-// The widest vector, up to 16 bytes, that divides every number in `at` (element strides, lengths) and the addresses.
+// The widest vector that divides every number in `at` (element strides, lengths) and the addresses, of those that kernels are
+// built for: 16 bytes, two values, one.
 inline int widest(bool bf16, std::initializer_list<int64_t> at, std::initializer_list<const void*> addresses)
 {
     const int es = bf16 ? 2 : 4;
@@ -87,7 +88,7 @@ inline int widest(bool bf16, std::initializer_list<int64_t> at, std::initializer
         while (n % v != 0) v /= 2;
     for (const void* p : addresses)
         while (reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(v * es) != 0) v /= 2;
-    return v;
+    return bf16 && v == 4 ? 2 : v;
 }
 
 template <bool BF, int V>

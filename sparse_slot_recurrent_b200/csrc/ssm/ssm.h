@@ -97,7 +97,6 @@ struct SsmParams {
     ChunkTok* toks;    // [B,H,ceil(T/64)], the tensor-core form only
     uint32_t* status;
     int poll_cost;  // of a wait of the tensor-core form: what one poll takes of the kWaitNs that it may last
-    int64_t chain_first;  // first (sequence, head) of a launch of the chaining kernel
 };
 
 struct SsmStepParams {

@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
     for (int k = threadIdx.x >> 5; k < n; k += 8) {  // a warp per piece
         if (p.toks) {
             const int chunks = (p.T + kChunk - 1) / kChunk, per = p.split.piece_len() / kChunk;
-            const int b = static_cast<int>((bh + p.chain_first) / p.H);
+            const int b = static_cast<int>(bh / p.H);
             const int have = (seq_len(p.lengths, b, p.T) + kChunk - 1) / kChunk;  // chunks that the sequence has
             double sum = 0.0;
             for (int i = k * per + (threadIdx.x & 31); i < min((k + 1) * per, have); i += 32) sum += p.toks[bh * chunks + i].total;
@@ -425,22 +425,11 @@ cudaError_t shape(const SsmParams& p, cudaStream_t s)
 
 }  // namespace
 
+// (Sequences are cut only where they are few: 148 blocks of four heads, or of 64 threads of 512 per SM, at most some hundreds.)
 cudaError_t launch_ssm_chain(const SsmParams& p, cudaStream_t s)
 {
-    const int64_t bh = static_cast<int64_t>(p.B) * p.H;
-    for (int64_t at = 0; at < bh; at += 65535) {  // the grid's limit in y
-        SsmParams q = p;
-        const int64_t np = static_cast<int64_t>(p.N) * p.P;
-        if (p.S_in) q.S_in = p.S_in + at * np;
-        q.seg_state = p.seg_state + at * p.split.slots() * np;
-        q.seg_decay = p.seg_decay + at * p.split.pieces();
-        if (p.toks) q.toks = p.toks + at * ((p.T + kChunk - 1) / kChunk);
-        q.chain_first = at;
-        const int64_t rows = bh - at < 65535 ? bh - at : 65535;
-        const cudaError_t e = launch_dependent(k_ssm_chain, dim3(static_cast<unsigned>((np / 4 + 255) / 256), static_cast<unsigned>(rows)), 256, 0, s, q);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    const unsigned heads = static_cast<unsigned>(p.B) * p.H;
+    return launch_dependent(k_ssm_chain, dim3(static_cast<unsigned>((p.N * p.P / 4 + 255) / 256), heads), 256, 0, s, p);
 }
 
 // As many segments as fill 148 SMs with one block of 128 channels each, none shorter than 256 tokens, and none at all
