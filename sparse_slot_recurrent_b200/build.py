@@ -3,7 +3,8 @@
 nvcc cross-compiles for sm_100a without a GPU.  The CUDA runtime is linked statically,
 so the library does not depend on which libcudart the host process (e.g. torch) loads.
 ``build(debug=True)`` builds ``libramnet_debug.so`` with RAMNET_DEBUG defined: every kernel
-then range-checks the slot, ring and event indices it computes and records a failed check
+then range-checks the slot, ring and event indices it computes (in the state space layer the
+rows, channels, segments and workspace places) and records a failed check
 in the status word (ramnet_sync_status reports RAMNET_ERR_DEVICE_CHECK) instead of making
 the access.
 """

@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(128, V > 1 ? 4 : 1) k_conv(ConvParams p, int n
     if (p.lengths) len = min(max(p.lengths[b], 0), p.T);
     if (t0 >= len && t0 > 0) return;
     const int t1 = min(t0 + run_len, len);
+    if (!dcheck(b < p.B && c + V <= p.C && t0 >= 0 && t1 <= p.T, p.status)) return;
     constexpr int H = (V + 1) / 2;            // pairs of channels
     constexpr int kBytes = Raw<IB, V>::kBytes;
     constexpr bool kRing = kBytes >= 4;       // what copies itself; a lone bf16 value comes through registers
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(128) k_conv_step(ConvStepParams p, int ncv, in
     if (id >= work) return;
     const int c = static_cast<int>(id % ncv) * V;
     const int64_t b = id / ncv;
+    if (!dcheck(b < p.B && c + V <= p.C, p.status)) return;
     const int64_t sbase = b * (W - 1) * p.C + c;
     Raw<IB, V> in[W];
 #pragma unroll

@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(128, 4) k_norm_warp(NormParams p)
     const int lane = threadIdx.x & 31;
     const int64_t row = id / p.groups;
     const int width = p.D / p.groups, first = static_cast<int>(id % p.groups) * width, nv = width / V;
+    if (!dcheck(row < p.R && first + width <= p.D && nv * V == width && nv <= 32 * NV, p.status)) return;
     Raw<IB, V> x[NV], z[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(kThreads) k_norm_block(NormParams p)
     constexpr int H = (V + 1) / 2;
     const int64_t row = blockIdx.x / p.groups;
     const int width = p.D / p.groups, first = static_cast<int>(blockIdx.x % p.groups) * width, nv = width / V;
+    if (!dcheck(row < p.R && first + width <= p.D && nv * V == width, p.status)) return;
     Val<V> u[NV][H], gate[NV][H];
 
     auto fetch = [&](int i, Val<V> (&uu)[H], Val<V> (&gg)[H]) {

@@ -22,6 +22,7 @@ struct ConvParams {
     int out_bf16;
     void* state_out;  // [B,W-1,C] or null; may alias state_in
     int B, T, C, W;
+    uint32_t* status;
 };
 
 struct ConvStepParams {
@@ -35,6 +36,7 @@ struct ConvStepParams {
     void* y;      // [B,C]
     int out_bf16;
     int B, C, W;
+    uint32_t* status;
 };
 
 // Element strides of one [B,T,H,.] operand (last dimension contiguous).
@@ -118,6 +120,7 @@ struct SsmStepParams {
     int B, H, G, N, P;
     int softplus;
     float dt_min, dt_max;
+    uint32_t* status;
 };
 
 struct NormParams {
@@ -133,6 +136,7 @@ struct NormParams {
     int D, groups;
     float eps;
     int gate_first;
+    uint32_t* status;
 };
 
 // Device address of the library's status word on the current device (null on a CUDA error).

@@ -32,6 +32,16 @@ bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 bool valid_dtype(ramnet_dtype d) { return d == RAMNET_F32 || d == RAMNET_BF16; }
 size_t elem(ramnet_dtype d) { return d == RAMNET_BF16 ? 2 : 4; }
 
+// The status word for kernels that only record failed range checks, of the build that makes these.
+uint32_t* check_word()
+{
+#ifdef RAMNET_DEBUG
+    return ramnet::library_status_word();
+#else
+    return nullptr;
+#endif
+}
+
 #define CHECK(cond, ...)                                            \
     do {                                                            \
         if (!(cond)) return fail(RAMNET_ERR_INVALID_ARG, __VA_ARGS__); \
@@ -191,7 +201,7 @@ ramnet_status ramnet_ssm_step(const ramnet_ssm_config* cfg, int32_t B, ramnet_dt
     NEED(y, 16);
     p.x = x, p.dt = dt, p.A = A, p.Bm = Bm, p.Cm = Cm, p.D = D, p.dt_bias = dt_bias;
     p.in_bf16 = in_dt == RAMNET_BF16, p.out_bf16 = out_dt == RAMNET_BF16;
-    p.S = S, p.y = y;
+    p.S = S, p.y = y, p.status = check_word();
     p.B = B, p.H = cfg->H, p.G = cfg->G, p.N = cfg->N, p.P = cfg->P;
     p.softplus = cfg->dt_softplus != 0, p.dt_min = cfg->dt_min, p.dt_max = cfg->dt_max;
     return launched(ramnet::launch_ssm_step(p, static_cast<cudaStream_t>(stream)), "ssm_step launch");
@@ -223,7 +233,7 @@ ramnet_status ramnet_conv_forward(int32_t B, int32_t T, int32_t C, int32_t W, ra
     MAY(state_out, 16);
     NEED(y, 16);
     ramnet::ConvParams p{x, x_b, x_t, in_dt == RAMNET_BF16, w, bias, silu != 0, lengths, state_in, y,
-                         out_dt == RAMNET_BF16, state_out, B, T, C, W};
+                         out_dt == RAMNET_BF16, state_out, B, T, C, W, check_word()};
     return launched(ramnet::launch_conv(p, static_cast<cudaStream_t>(stream)), "conv_forward launch");
 }
 
@@ -245,7 +255,7 @@ ramnet_status ramnet_conv_step(int32_t B, int32_t C, int32_t W, ramnet_dtype in_
     MAY(bias, 4);
     NEED(state, 16);
     NEED(y, 16);
-    ramnet::ConvStepParams p{x, x_b, in_dt == RAMNET_BF16, w, bias, silu != 0, state, y, out_dt == RAMNET_BF16, B, C, W};
+    ramnet::ConvStepParams p{x, x_b, in_dt == RAMNET_BF16, w, bias, silu != 0, state, y, out_dt == RAMNET_BF16, B, C, W, check_word()};
     return launched(ramnet::launch_conv_step(p, static_cast<cudaStream_t>(stream)), "conv_step launch");
 }
 
@@ -269,7 +279,7 @@ ramnet_status ramnet_norm_gate(int64_t R, int32_t D, int32_t groups, ramnet_dtyp
     MAY(z, es);
     MAY(w, 16);
     NEED(y, 16);
-    ramnet::NormParams p{x, x_r, z, z_r, in_dt == RAMNET_BF16, w, y, out_dt == RAMNET_BF16, R, D, groups, eps, gate_first != 0};
+    ramnet::NormParams p{x, x_r, z, z_r, in_dt == RAMNET_BF16, w, y, out_dt == RAMNET_BF16, R, D, groups, eps, gate_first != 0, check_word()};
     return launched(ramnet::launch_norm_gate(p, static_cast<cudaStream_t>(stream)), "norm_gate launch");
 }
 

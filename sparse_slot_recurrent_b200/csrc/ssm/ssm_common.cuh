@@ -49,6 +49,13 @@ __device__ __forceinline__ SegRange seg_range(int len, int seg, int seg_len)
     return r;
 }
 
+// Whether a range lies within its sequence, and its state among the workspace's (outputs by segment, else by piece).
+__device__ __forceinline__ bool segment_fits(const SsmParams& p, const SegRange& r, int seg, bool outputs)
+{
+    const int at = outputs ? seg * p.split.sub : seg;
+    return 0 <= r.first && r.first <= r.last && r.last <= p.T && at < p.split.slots() && seg < (outputs ? p.split.nseg : p.split.pieces());
+}
+
 // 2^x, rounded once: a bias of the hardware's exp2, a fraction of an ulp, would add up over the hundreds of
 // chunks that a slowly decaying state remembers.  Taylor series of 2^f, |f| <= 1/2, in 64 bits (error below 1e-11).
 __device__ __forceinline__ float exp2_of(double x)

@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(PT * (N / NR)) k_ssm_scan(SsmParams p)
     const int64_t b = bh / p.H;
     const int g = h / (p.H / p.G);
     const SegRange r = seg_range(seq_len(p.lengths, static_cast<int>(b), p.T), seg, OUT ? p.split.seg_len : p.split.piece_len());
+    if (!dcheck(b < p.B && g < p.G && (tile + 1) * PT <= p.P && segment_fits(p, r, seg, OUT), p.status)) return;
     const int s = tid % NS, pl = tid / NS;
     const int ch = tile * PT + pl;
     const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f, skip = p.D ? p.D[h] : 0.0f;
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(N / 8 * (PT / 4)) k_ssm_tile(SsmParams p)
     const int64_t b = bh / p.H;
     const int g = h / (p.H / p.G);
     const SegRange r = seg_range(seq_len(p.lengths, static_cast<int>(b), p.T), seg, OUT ? p.split.seg_len : p.split.piece_len());
+    if (!dcheck(b < p.B && g < p.G && (tile + 1) * PT <= p.P && segment_fits(p, r, seg, OUT), p.status)) return;
     const int s = tid % NG, pl = tid / NG * 4;  // lane's place among the state values; its first channel
     const int64_t np = static_cast<int64_t>(N) * p.P;
     const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f, skip = p.D ? p.D[h] : 0.0f;
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__(256) k_ssm_chain(SsmParams p)
     const int e = blockIdx.x * 256 + threadIdx.x;
     const int64_t bh = blockIdx.y;
     const int n = p.split.pieces(), sub = p.split.sub;
+    if (!dcheck(bh < static_cast<int64_t>(p.B) * p.H && n <= 256 && sub > 0 && n % sub == 0, p.status)) return;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), add = s;
     float4* at = reinterpret_cast<float4*>(p.seg_state) + bh * p.split.slots() * np4 + e;
     if (e < np4) {  // on their way while the decays are summed

@@ -106,6 +106,7 @@ __global__ void __launch_bounds__(256) k_ssm_decay(const SsmParams p, int chunks
     const int c = static_cast<int>(bc % chunks), b = static_cast<int>(bc / chunks);
     const int len = seq_len(p.lengths, b, p.T), t0 = c * kQ;
     if (t0 >= len) return;
+    if (!dcheck(b < p.B && len <= p.T, p.status)) return;
     const float bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
     const double A = static_cast<double>(p.A[h]) * 1.4426950408889634074;
     float d[2];
@@ -201,6 +202,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
     const int nch = (r.last - r.first + kQ - 1) / kQ;
     const bool ragged = (r.last - r.first) % kQ != 0;  // the last chunk is not full
     const int head0 = c0 / P;                          // first head, within the group
+    // (segments start with a chunk; the workspace holds (T + 63) / 64 of them per head)
+    if (!dcheck(b < p.B && c0 < cend && head0 < hg && segment_fits(p, r, seg, OUT) && (nch == 0 || r.first % kQ == 0) &&
+                    r.first / kQ + nch <= (p.T + kQ - 1) / kQ, p.status))
+        return;
 
     auto bar = [&](int i) { return bars + 8u * i; };
     auto wait = [&](int i, uint32_t parity) { wait_phase(bars + 8u * i, parity, limit_addr); };

@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(TH) k_ssm_step(SsmStepParams p)
     const int N = p.N, P = p.P, lp = P / 4;  // threads per state row
     const int nrow = TH / lp;                // rows per pass of the block
     const int c = threadIdx.x % lp, r0 = threadIdx.x / lp;
+    if (!dcheck(b < p.B && g < p.G && N <= 256 && lp * nrow == TH && nrow > 0, p.status)) return;
     float* S = p.S + (b * p.H + h) * static_cast<int64_t>(N) * P;
 
     float4 s[kRows];
