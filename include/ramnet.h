@@ -388,8 +388,8 @@ ramnet_status ramnet_conv_step(int32_t B, int32_t C, int32_t W, ramnet_dtype in_
  * ramnet_norm_gate -- RMSNorm of R rows over groups of D/groups channels, with a SiLU gate:
  *     gate_first != 0:  u = x * silu(z),  y = u / sqrt(mean_group(u^2) + eps) * w
  *     gate_first == 0:  y = x / sqrt(mean_group(x^2) + eps) * w * silu(z)
- *   x, z [R,D] in_dt with row strides x_r, z_r in elements (z NULL: no gate);  w [D] fp32 or
- *   NULL (ones);  y [R,D] out_dt, dense
+ *   x, z [R,D] in_dt with row strides x_r, z_r in elements (z NULL: no gate);  w [D] fp32,
+ *   16-byte aligned, or NULL (ones);  y [R,D] out_dt, dense
  * Limits: R*groups < 2^31, D <= 2^30.  Errors: INVALID_ARG.
  */
 ramnet_status ramnet_norm_gate(int64_t R, int32_t D, int32_t groups, ramnet_dtype in_dt, const void* x,

@@ -106,8 +106,9 @@ __device__ __forceinline__ void store_vec(void* base, int64_t i, const float (&v
     }
 }
 
-// SiLU.  For a bf16 result the hardware's exp2 and reciprocal are enough (their relative error
-// of about 2^-21 is far below bf16's 2^-9); an fp32 result takes the accurate forms.
+// SiLU.  For a bf16 result the hardware's exp2 and reciprocal are enough: they are off by about 2^-21 of the value, and for
+// negative p the rounding of the exponent by |p| 2^-24 more (2^-17.7 at p = -80), against bf16's 2^-9; below p = -87,
+// where the value is under 1e-36, they give 0.  An fp32 result takes the accurate forms.
 template <bool FAST>
 __device__ __forceinline__ F2 silu2(F2 p)
 {

@@ -17,7 +17,8 @@
 // Precision.  The state itself stays in fp32 registers and takes dS with one fused multiply-add
 // per chunk (the tensor core's accumulation would shave a bit off a long-lived state every
 // chunk).  Xw is exact in three pieces of 8 bits.  As operands of a bf16 result W and S carry two pieces: 2^-16 of each
-// value, against the result's own 2^-9.  Sums of d A are taken in 64 bits; a_i - a_j is the
+// value, against the result's own 2^-9 (0.3% of the results become the neighbouring bf16 value; the error against 64 bits is
+// 1.658e-3 either way, the rounding of the result).  Sums of d A are taken in 64 bits; a_i - a_j is the
 // difference of two float pairs within a block of 16 tokens, and between blocks a product of factors that meet at
 // block ends, so strong decay early in a chunk costs later tokens nothing.
 //
@@ -30,15 +31,17 @@
 //
 // What is no number spreads forward in time only.  B, C and step sizes meet other tokens through W alone, whose upper triangle
 // is selected, not multiplied; but x_j meets every W[i,j] of its chunk in Ya, and 0 NaN is NaN.  So x that is no number is
-// taken as 0, and its channel's outputs and final state from that token on are set to NaN.
+// taken as 0, and its channel's outputs and final state from that token on are set to NaN.  (Looking for it costs 2% of a
+// prompt's time; 20% where a warp of its own reads every chunk of x for it before the others may.)
 //
 // The code of all roles has to stay within the instruction cache: with the loops fully unrolled (72 KB) every role
 // waited for instructions and a prompt took a third longer; unrolling W alone costs 3%.
-// Measured, B4 T16384 H16 P128 N128: 315 us (574 MB: 87 us at the copy bandwidth; token by token in registers 14 ms).
+// Measured, B4 T16384 H16 P128 N128: 318 us over one set of inputs, 360 to 373 over sets in turn (574 MB: 87 us at the copy
+// bandwidth; token by token in registers 14 ms).
 // About 3700 cycles per chunk, of which the tensor pipe works 1900, shared memory 2100, HBM 1400.  Bound: the
 // operand warps of the first quadrant, whose diagonal and off-diagonal blocks of W take 1300 cycles of issue and latency
 // between a chunk's G and its Ya.
-// B8 T4096 H8 P128 N128: 95 us with 2 segments per sequence; B6 T1021 H24 P64 N64 in 2 groups: 37 us.
+// B8 T4096 H8 P128 N128: 94 to 105 us with 2 segments per sequence; B6 T1021 H24 P64 N64 in 2 groups: 39 to 42 us.
 #include <climits>
 
 #include "ssm_mma.cuh"
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_ssm_mma(const __grid_constant__
                     }
                 }
                 fence_async_smem();
-                uint32_t sum[2] = {0, 0};  // (here, since the loads of x have long ended: 3% less than in front of W)
+                uint32_t sum[2] = {0, 0};  // (here, since the loads of x have long ended: 2% less than in front of W)
 #pragma unroll
                 for (int k = 0; k < 16; ++k) add_zeros(sum[k & 1], x[k >> 3][(k >> 2) & 1][k & 3]);
                 if (__any_sync(0xffffffffu, ((sum[0] | sum[1]) & 0x7fff7fffu) != 0)) {

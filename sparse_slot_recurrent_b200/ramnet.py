@@ -569,8 +569,8 @@ def conv_step(x, w, state, bias=None, silu=True, out_dtype=None, y=None, stream=
 
 
 def norm_gate(x, z=None, w=None, groups=1, eps=1e-6, gate_first=True, out_dtype=None, y=None, stream=None):
-    """RMSNorm of the rows of x [R,D] over ``groups`` groups of channels, times w [D] fp32, gated by silu(z)
-    (z [R,D], None: no gate) before the norm or behind it.  Returns y [R,D]."""
+    """RMSNorm of the rows of x [R,D] over ``groups`` groups of channels, times w [D] fp32 (starting on 16 bytes),
+    gated by silu(z) (z [R,D], None: no gate) before the norm or behind it.  Returns y [R,D]."""
     R, D = x.shape
     if D > _MAX or not -_MAX <= groups <= _MAX:
         _fits(D=D, groups=groups)
