@@ -359,7 +359,8 @@ def decode_step(cfg: Config, k_logits, q_logits, v, g, z, S, m, pos=None, norm_w
     """One decode token per (b,h); S [B,H,M,d_v] and m [B,H,M] fp32 are updated in place.
     Returns y [B,H,d_v]."""
     B, H, L = k_logits.shape
-    _fits(B=B, H=H)
+    if B > _MAX or H > _MAX:
+        _fits(B=B, H=H)
     _dense(k_logits, q_logits, v, g, z, S, m, pos, norm_w, cape_mask)
     if y is None:
         y = torch.empty((B, H, cfg.d_v), dtype=out_dtype, device=k_logits.device)
