@@ -378,7 +378,7 @@ def selftest_wait_timeout(limit_us: int, stream=None):
 
 
 def set_scan_wait_limit(limit_us: int):
-    """Limit of the prefill recurrence's bounded waits for later launches (0: 2 s default)."""
+    """Limit of the bounded waits of the prefill recurrence and the selective scan for later launches (0: 2 s default)."""
     _fits(limit_us=limit_us)
     _check(load().ramnet_set_scan_wait_limit(limit_us))
 
